@@ -34,6 +34,10 @@ EXPORTS = (
     "zo_debug_cell_preact", "zo_profile", "zo_profile_read", "zo_probe_losses_static",
     "zo_probe_losses_slice", "zo_loss", "zo_coeffs_forward", "zo_debug_cell_stall",
     "zo_debug_cell_variant",
+    "zo_conv", "zo_conv_step", "zo_conv_backward_workspace", "zo_conv_backward",
+    "zo_scan_workspace", "zo_scan_backward_workspace", "zo_scan", "zo_scan_step",
+    "zo_scan_backward", "zo_block_norm", "zo_block_norm_backward_workspace",
+    "zo_block_norm_backward",
 )
 ZO_CELL_SINGLE, ZO_CELL_SINGLE_EXACT_EPS, ZO_CELL_PAIR, ZO_CELL_PAIR_EXACT_EPS, \
     ZO_CELL_PAIR_DIRECT_W, ZO_CELL_SINGLE_EPI8 = 0, 1, 2, 3, 4, 5
@@ -99,6 +103,7 @@ def load_library(path: str = LIB_PATH):
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = res
+    block.declare(lib)
     _lib = lib
     return lib
 
@@ -305,3 +310,11 @@ def cdrge_step(ctx, theta, step_seed, n_pert, eps, eta, tokens, targets, loss_pl
                     stream=stream)
     zo_coeffs(ctx, loss_plus, loss_minus, n_pert, eps, eta, coeffs, stream=stream)
     zo_update(ctx, theta, step_seed, n_pert, coeffs, stream=stream)
+
+
+from . import block  # noqa: E402  (its calls use the definitions above)
+from .block import (  # noqa: E402,F401
+    ZO_CONV_SILU, ZO_DTYPE_FP16, ZO_MAX_NORM_WIDTH, ZO_MAX_STATES, ZO_MAX_TAPS,
+    ZO_NORM_GATE_FIRST, ZO_SCAN_CHUNK, ZO_SCAN_SOFTPLUS, zo_block_norm, zo_block_norm_backward,
+    zo_conv, zo_conv_backward, zo_conv_step, zo_scan, zo_scan_backward, zo_scan_checkpoint_shape,
+    zo_scan_step)

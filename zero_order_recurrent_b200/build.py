@@ -19,6 +19,7 @@ NVCC_FLAGS = [
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "--expt-relaxed-constexpr",
+    "--threads", "0",
     "-shared",
 ]
 
@@ -34,7 +35,7 @@ def sources():
 
 def _inputs():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        [os.path.join(ROOT, "include", "zo.h")]
+        glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
 def stale() -> bool:
