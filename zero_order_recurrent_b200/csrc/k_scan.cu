@@ -148,73 +148,7 @@ __device__ __forceinline__ void store_states4(float* p, int n0, int N, const flo
   }
 }
 
-__device__ __forceinline__ void store_states(float* p, int n0, int N, const float2 (&h)[2]) {
-  const float f[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
-  if (N % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0)
-    store_states4<true>(p, n0, N, f);
-  else
-    store_states4<false>(p, n0, N, f);
-}
-
 // ---- forward -------------------------------------------------------------------
-
-// Lanes: the 32 / LN channels of a warp are neighbours and a channel's LN lanes
-// 32 / LN apart.  A shared-memory access of 16 bytes a lane takes two clocks when
-// neighbouring lanes ask for the same address (B and C here) and four when they
-// do not; the other order made those the bound.
-template <int LN>
-constexpr int kWidth = 32 / LN;
-
-// Sum over the LN lanes of a channel of y[j], j < min(LN, 4) steps: exchanges
-// that halve the number of steps a lane keeps, then plain ones.  Lane q of the
-// channel gets the sum of step q % 4 (q % LN for fewer lanes).
-template <int LN>
-constexpr int steps_per_sum() {
-  return LN < 4 ? LN : 4;
-}
-
-template <int LN>
-__device__ __forceinline__ float sum_steps(const float (&y)[steps_per_sum<LN>()], int q) {
-  constexpr int W = kWidth<LN>;
-  float v;
-  if constexpr (LN == 1) {
-    v = y[0];
-  } else if constexpr (LN == 2) {
-    const float keep = q & 1 ? y[1] : y[0], give = q & 1 ? y[0] : y[1];
-    v = keep + __shfl_xor_sync(0xffffffffu, give, W);
-  } else {
-    float k0 = q & 1 ? y[1] : y[0], g0 = q & 1 ? y[0] : y[1];
-    float k1 = q & 1 ? y[3] : y[2], g1 = q & 1 ? y[2] : y[3];
-    k0 += __shfl_xor_sync(0xffffffffu, g0, W);
-    k1 += __shfl_xor_sync(0xffffffffu, g1, W);
-    v = (q & 2 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, q & 2 ? k0 : k1, 2 * W);
-#pragma unroll
-    for (int m = 4; m < LN; m *= 2) v += __shfl_xor_sync(0xffffffffu, v, m * W);
-  }
-  return v;
-}
-
-// A tile of time in shared memory.
-template <class T, int LN, int WT, int WC>
-struct Tile {
-  static constexpr int kSteps = kChunk * WT;
-  static constexpr int kChannels = WC * kWidth<LN>;
-  static constexpr int kThreads = 32 * WT * WC;
-  static constexpr int kStates = 4 * LN;
-  // as in memory, on their way while the tile before is computed
-  alignas(16) T u[kSteps][kChannels];
-  alignas(16) T d[kSteps][kChannels];
-  alignas(16) T z[kSteps][kChannels];
-  alignas(16) T b[kSteps][kStates];
-  alignas(16) T c[kSteps][kStates];
-  // what the scan reads
-  alignas(16) float2 dx[kSteps][kChannels];   // d, d u (0 behind the row's length)
-  alignas(16) float2 out[kSteps][kChannels];  // skip u, silu(z)
-  alignas(16) float B[kSteps][kStates], C[kSteps][kStates];
-  // what the time warps exchange (WT > 1)
-  float decay[WT][kChannels][kStates], state[WT][kChannels][kStates], end[kChannels][kStates];
-  alignas(16) float2 set[kChannels];  // delta's bias, skip
-};
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
@@ -230,13 +164,13 @@ __device__ __forceinline__ void copies_done() {
 
 // Copies `steps` rows of the first `width` of PITCH elements, asynchronously
 // `bytes` at a time (16, 8 or 4, which divide a row; 0: element by element).
-template <class T, int PITCH, int THREADS>
+template <class T, int PITCH>
 __device__ __forceinline__ void fetch_rows(T* to, const T* from, int64_t step, int steps, int width,
                                            int bytes) {
   auto run = [&](auto size) {
     constexpr int B = decltype(size)::value, E = B / (int)sizeof(T), P = PITCH / E;
     if constexpr (E >= 1 && P >= 1) {
-      for (int i = threadIdx.x; i < steps * P; i += THREADS) {
+      for (int i = threadIdx.x; i < steps * P; i += blockDim.x) {
         const int t = i / P, c = i % P * E;
         if (c < width) copy_async<B>(to + t * PITCH + c, from + t * step + c);
       }
@@ -249,237 +183,292 @@ __device__ __forceinline__ void fetch_rows(T* to, const T* from, int64_t step, i
   else if (bytes == 4)
     run(std::integral_constant<int, 4>());
   else
-    for (int i = threadIdx.x; i < steps * PITCH; i += THREADS) {
+    for (int i = threadIdx.x; i < steps * PITCH; i += blockDim.x) {
       const int t = i / PITCH, c = i % PITCH;
       if (c < width) to[i] = from[t * step + c];
     }
 }
 
-// Blocks of an SM that the registers must allow.
-template <int LN, int WT>
-constexpr int scan_residency() {
-  return WT == 1 ? (LN < 16 ? 6 : 4) : 2;
+// S states from n0 on, as S / 2 pairs.
+template <int S>
+__device__ __forceinline__ void load_pairs(const float* p, int n0, int N, bool wide, float2 (&h)[S / 2]) {
+#pragma unroll
+  for (int i = 0; i < S; i += 4) {
+    float f[4];
+    if (wide)
+      load_states4<true>(p, n0 + i, N, f);
+    else
+      load_states4<false>(p, n0 + i, N, f);
+    h[i / 2] = make_float2(f[0], f[1]);
+    h[i / 2 + 1] = make_float2(f[2], f[3]);
+  }
 }
 
-// WT warps divide a tile of time among them (kChunk steps each) and WC warps its
-// channels.  With WT > 1 every warp first runs its steps from the state 0 and
-// keeps their decays exp(d A) in registers; the warps then exchange (decay of
-// the whole chunk, state at its end), so each knows the state that it starts
-// from, and run the steps again, this time without exponentials.  That costs one
-// more multiply-add a state and step and makes WT times as many warps, which a
-// few long rows need to fill the SMs.
-//
-// A block walks the tiles of `rows` rows of one set, one row after the other;
-// the next tile's inputs are on their way while a tile is computed.
+template <int S>
+__device__ __forceinline__ void store_pairs(float* p, int n0, int N, bool wide, const float2 (&h)[S / 2]) {
+#pragma unroll
+  for (int i = 0; i < S; i += 4) {
+    const float f[4] = {h[i / 2].x, h[i / 2].y, h[i / 2 + 1].x, h[i / 2 + 1].y};
+    if (wide)
+      store_states4<true>(p, n0 + i, N, f);
+    else
+      store_states4<false>(p, n0 + i, N, f);
+  }
+}
+
+// How time is divided among blocks: `n` parts of `steps` steps (whole chunks).
+// Part k starts from state[row][k] and sum[row][k] holds its sum of d.
+struct Parts {
+  int n, steps;
+  float *state, *sum;
+};
+
+constexpr int kTile = kChunk;  // steps of B and C in shared memory
+
+template <class T, int NP>
+struct BC {
+  alignas(16) T raw[2][2][kTile][NP];     // [buffer][B, C]: as in memory, on their way
+  alignas(16) float f[2][2][kTile][NP];   // [buffer][B, C]: what the scan reads
+};
+
+// A lane holds S states of one channel (LN lanes a channel where there are more
+// than 16), a warp 32 / LN neighbouring channels, and everything of a channel and
+// step - softplus, silu, loads, the output - is done once, by that lane.  B and C,
+// which all channels of a group share, come through shared memory a tile ahead;
+// u, delta and z come straight into registers kAhead steps ahead.
 //
 // Bound: the special function unit, 16 results a clock and SM.  A value with 16
-// states needs 16 exponentials and 5 for softplus and silu, 21 / 16 clocks; its
-// 8 bytes in bf16 take 0.34 clocks of an SM's share of the memory.
-template <class T, int LN, int WT, int WC>
-__global__ void __launch_bounds__(32 * WT * WC, scan_residency<LN, WT>())
-    scan_kernel(zo_scan_args a, ScanDims d, int rows, int copy, int copy_bc) {
-  using S = Tile<T, LN, WT, WC>;
+// states takes 16 exponentials and 5 for softplus and silu, so 21 / 16 clocks; its
+// 8 bytes in bf16 take 0.34 clocks of an SM's share of the memory.  The 16
+// exponentials of one step are independent, so a warp a scheduler nearly fills the
+// unit.  Fewer lanes a state (four states a lane) make more warps, but were bound
+// by shared-memory accesses and issue: 2.5 times the instructions a value.
+//
+// Where rows and channels are too few for the SMs, time is divided as well: LOCAL
+// runs each part but the last from the state 0, scan_join_kernel passes the states
+// on from part to part, and then all parts run from the states they start with.
+// That takes the exponentials twice.
+//
+// A block takes `rows` rows of one set one after the other.
+constexpr int kAhead = 4;
+
+template <class T, int S, int LN, bool LOCAL>
+__global__ void __launch_bounds__(128, 4)
+    scan_kernel(zo_scan_args a, ScanDims d, Parts parts, int rows, int copy_bc, bool wide) {
+  constexpr int NP = S * LN, W = 32 / LN, H = S / 2;
   extern __shared__ __align__(16) unsigned char smem[];
-  S& sh = *reinterpret_cast<S*>(smem);
-  const unsigned tiles = d.tiles * d.G, blocks = (d.rows_per_set + rows - 1) / rows;
-  const unsigned tile_g = blockIdx.x % tiles, rest = blockIdx.x / tiles;
+  BC<T, NP>& sh = *reinterpret_cast<BC<T, NP>*>(smem);
+  const unsigned tiles = d.tiles * d.G, row_blocks = (d.rows_per_set + rows - 1) / rows;
+  const unsigned nparts = LOCAL ? parts.n - 1 : parts.n;
+  const unsigned tile_g = blockIdx.x % tiles, r1_ = blockIdx.x / tiles;
+  const int part = r1_ % nparts;
+  const unsigned rest = r1_ / nparts;
   const int tile = tile_g % d.tiles, g = tile_g / d.tiles;
-  const int set = rest / blocks, first = (int)(rest % blocks) * rows;
+  const int set = rest / row_blocks, first = (int)(rest % row_blocks) * rows;
   const int row0 = set * d.rows_per_set + first;
   const int row1 = row0 + (first + rows < d.rows_per_set ? rows : d.rows_per_set - first);
+  const int tb = part * parts.steps, te = tb + parts.steps < d.T ? tb + parts.steps : (int)d.T;
 
-  const int tid = threadIdx.x, warp = tid / 32, wt = warp % WT, wc = warp / WT;
-  const int q = tid % 32 / kWidth<LN>, n0 = q * 4, ch = wc * kWidth<LN> + tid % kWidth<LN>;
-  const int left = d.Dg - tile * S::kChannels;  // channels of the group from the tile on
-  const bool on = ch < left;
-  const int64_t c0 = (int64_t)g * d.Dg + tile * S::kChannels;
-  const int T_ = (int)d.T;
-  float2 A2[2];
-  {
-    float A[4] = {0.f, 0.f, 0.f, 0.f};
-    if (on) load_states(a.A.ptr + set * a.A.stride + (c0 + ch) * d.N, n0, d.N, A);
-    A2[0] = make_float2(A[0] * kLog2e, A[1] * kLog2e);
-    A2[1] = make_float2(A[2] * kLog2e, A[3] * kLog2e);
-  }
-  const bool softplus = a.flags & ZO_SCAN_SOFTPLUS, gate = a.z.ptr != nullptr;
-  if (tid < S::kChannels)
-    sh.set[tid] = make_float2(
-        a.delta_bias.ptr && tid < left ? a.delta_bias.ptr[set * a.delta_bias.stride + c0 + tid] : 0.f,
-        a.skip.ptr && tid < left ? a.skip.ptr[set * a.skip.stride + c0 + tid] : 0.f);
+  const int lane = threadIdx.x % 32, q = lane / W, n0 = q * S;
+  const int k = (tile * (int)(blockDim.x / 32) + (int)threadIdx.x / 32) * W + lane % W;
+  const bool on = k < d.Dg;
+  const int64_t c = (int64_t)g * d.Dg + (on ? k : 0);
+  float2 A2[H];
+  load_pairs<S>(a.A.ptr + set * a.A.stride + c * d.N, n0, d.N, false, A2);
+#pragma unroll
+  for (int i = 0; i < H; ++i) A2[i] = __fmul2_rn(A2[i], two(kLog2e));
+  const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[set * a.delta_bias.stride + c] : 0.f;
+  const float skip = !LOCAL && a.skip.ptr ? a.skip.ptr[set * a.skip.stride + c] : 0.f;
+  const bool softplus = a.flags & ZO_SCAN_SOFTPLUS, gate = !LOCAL && a.z.ptr;
 
-  // Sets the tile at step t0 of a row on its way; `valid` steps of it exist.
-  const int width = left < S::kChannels ? left : S::kChannels;
-  auto fetch = [&](int64_t row, int64_t t0, int valid) {
-    constexpr int C = S::kChannels, N = S::kStates, H = S::kThreads;
-    fetch_rows<T, C, H>(&sh.u[0][0], static_cast<const T*>(a.u.ptr) + row * a.u.row + t0 * a.u.step + c0,
-                        a.u.step, valid, width, copy);
-    fetch_rows<T, C, H>(&sh.d[0][0], static_cast<const T*>(a.delta.ptr) + row * a.delta.row + t0 * a.delta.step + c0,
-                        a.delta.step, valid, width, copy);
-    if (gate)
-      fetch_rows<T, C, H>(&sh.z[0][0], static_cast<const T*>(a.z.ptr) + row * a.z.row + t0 * a.z.step + c0,
-                          a.z.step, valid, width, copy);
+  const bool tell = tile == 0 && part == 0 && threadIdx.x == 0 && !LOCAL;
+  auto end_of = [&](int row) {  // of the part, or of the row where that comes first
+    const int n = (int)row_length(a.lengths, row, d.T, a.status, tell);
+    return n < te ? n : te;
+  };
+  // B and C of the tile at step t of a row
+  auto fetch = [&](int row, int t, int end, int buf) {
+    const int n = end - t < kTile ? end - t : kTile;
     const int64_t gn = (int64_t)g * d.N;
-    fetch_rows<T, N, H>(&sh.b[0][0], static_cast<const T*>(a.B.ptr) + row * a.B.row + t0 * a.B.step + gn,
-                        a.B.step, valid, d.N, copy_bc);
-    fetch_rows<T, N, H>(&sh.c[0][0], static_cast<const T*>(a.C.ptr) + row * a.C.row + t0 * a.C.step + gn,
-                        a.C.step, valid, d.N, copy_bc);
+    fetch_rows<T, NP>(&sh.raw[buf][0][0][0],
+                      static_cast<const T*>(a.B.ptr) + row * a.B.row + t * a.B.step + gn, a.B.step, n, d.N, copy_bc);
+    if (!LOCAL)
+      fetch_rows<T, NP>(&sh.raw[buf][1][0][0],
+                        static_cast<const T*>(a.C.ptr) + row * a.C.row + t * a.C.step + gn, a.C.step, n, d.N, copy_bc);
   };
-  // Steps of the tile at t0 that a row of length n has.
-  auto steps_of = [&](int n, int t0) { return n - t0 < S::kSteps ? n > t0 ? n - t0 : 0 : S::kSteps; };
-  auto load_state = [&](int64_t row, float2 (&h)[2]) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (on && a.state_in.ptr)
-      load_states(a.state_in.ptr + row * a.state_in.stride + (c0 + ch) * d.N, n0, d.N, s);
-    h[0] = make_float2(s[0], s[1]);
-    h[1] = make_float2(s[2], s[3]);
+  auto convert = [&](int buf) {  // states beyond N multiply zeros: h is 0 there
+    constexpr int M = (LOCAL ? 1 : 2) * kTile * NP / 4;
+    for (int i = threadIdx.x; i < M; i += blockDim.x) {
+      const int n = i % (NP / 4) * 4;
+      float f[4];
+      load_vec<T, 4>(&sh.raw[buf][0][0][0] + i * 4, f);
+      if (n + 4 > d.N)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j >= d.N) f[j] = 0.f;
+      store_vec<float, 4>(&sh.f[buf][0][0][0] + i * 4, f);
+    }
   };
-  const bool tell = tile == 0 && tid == 0;
-  int len = (int)row_length(a.lengths, row0, d.T, a.status, tell);
-  fetch(row0, 0, steps_of(len, 0));
-  float2 next[2];  // the next row's first state
-  load_state(row0, next);
+  T ru[kAhead], rd[kAhead], rz[kAhead];
+  const T *pu, *pd, *pz = nullptr;  // the next steps to load
+  auto at = [&](int row) {
+    pu = static_cast<const T*>(a.u.ptr) + row * a.u.row + tb * a.u.step + c;
+    pd = static_cast<const T*>(a.delta.ptr) + row * a.delta.row + tb * a.delta.step + c;
+    if (gate) pz = static_cast<const T*>(a.z.ptr) + row * a.z.row + tb * a.z.step + c;
+  };
+  auto load = [&](int n) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (j < n) {
+        ru[j] = pu[j * a.u.step];
+        rd[j] = pd[j * a.delta.step];
+        if (gate) rz[j] = pz[j * a.z.step];
+      }
+    pu += kAhead * a.u.step;
+    pd += kAhead * a.delta.step;
+    if (gate) pz += kAhead * a.z.step;
+  };
 
+  int end = end_of(row0), buf = 0;
+  at(row0);
+  load(end - tb);
+  fetch(row0, tb, end, 0);
   for (int row = row0; row < row1; ++row) {
-    float2 h[2] = {next[0], next[1]};
-    T* out = static_cast<T*>(a.out.ptr) + row * a.out.row + c0;
-    const int next_len = row + 1 < row1 ? (int)row_length(a.lengths, row + 1, d.T, a.status, tell) : 0;
-    for (int t0 = 0; t0 < T_; t0 += S::kSteps) {
-      const int steps = steps_of(T_, t0), valid = steps_of(len, t0);
-      const bool last = t0 + S::kSteps >= T_;
+    const bool more = row + 1 < row1;
+    const int next_end = more ? end_of(row + 1) : 0;
+    float2 h[H];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < H; ++i) h[i] = two(0.f);
+    if (!LOCAL) {
+      if (parts.n > 1)
+        load_pairs<S>(parts.state + (((int64_t)row * parts.n + part) * d.D + c) * d.N, n0, d.N, wide, h);
+      else if (a.state_in.ptr)
+        load_pairs<S>(a.state_in.ptr + row * a.state_in.stride + c * d.N, n0, d.N, wide, h);
+    }
+    T* out = LOCAL ? nullptr : static_cast<T*>(a.out.ptr) + row * a.out.row + tb * a.out.step + c;
+    int t = tb;
+    for (; t < end; t += kTile) {
       copies_done();
       __syncthreads();
-      if (valid == 0) {  // behind the row's end: zeros, and the state as it is
-        if (last && row + 1 < row1) {
-          fetch(row + 1, 0, steps_of(next_len, 0));
-          load_state(row + 1, next);
-        }
-        if (WT > 1 && len > 0) {  // a tile came before
-          const float4 e = *reinterpret_cast<const float4*>(&sh.end[ch][n0]);
-          h[0] = make_float2(e.x, e.y);
-          h[1] = make_float2(e.z, e.w);
-        }
-        if (on && a.checkpoints && wt * kChunk < steps)
-          store_states(a.checkpoints + ((row * d.chunks + t0 / kChunk + wt) * d.D + c0 + ch) * d.N,
-                       n0, d.N, h);
-        for (int i = tid; i < steps * S::kChannels; i += S::kThreads) {
-          const int t = i / S::kChannels, c = i % S::kChannels;
-          if (c < left) out[(t0 + t) * a.out.step + c] = from_f<T>(0.f);
-        }
-        continue;
-      }
-      // Everything that is one channel's and step's is computed once, for two
-      // channels at a time.
-      constexpr int P = S::kChannels / 2;
-#pragma unroll 2
-      for (int i = tid; i < S::kSteps * P; i += S::kThreads) {
-        const int t = i / P, c = i % P * 2;
-        float4 dx = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t < valid) {
-          const float4 k = *reinterpret_cast<const float4*>(&sh.set[c]);
-          const float2 u = make_float2(to_f(sh.u[t][c]), to_f(sh.u[t][c + 1]));
-          float2 dt = make_float2(to_f(sh.d[t][c]) + k.x, to_f(sh.d[t][c + 1]) + k.z);
-          if (softplus) dt = softplus_2(dt);
-          const float2 x = __fmul2_rn(dt, u), su = __fmul2_rn(make_float2(k.y, k.w), u);
-          const float2 sz = gate ? silu_2(make_float2(to_f(sh.z[t][c]), to_f(sh.z[t][c + 1]))) : two(1.f);
-          dx = make_float4(dt.x, x.x, dt.y, x.y);
-          *reinterpret_cast<float4*>(&sh.out[t][c]) = make_float4(su.x, sz.x, su.y, sz.y);
-        }
-        *reinterpret_cast<float4*>(&sh.dx[t][c]) = dx;  // of channels behind the last: not read
-      }
-#pragma unroll 2
-      for (int i = tid; i < S::kSteps * LN; i += S::kThreads) {
-        const int t = i / LN, n = i % LN * 4;
-        float fb[4] = {0.f, 0.f, 0.f, 0.f}, fc[4] = {0.f, 0.f, 0.f, 0.f};
-        if (t < valid) {
-          load_vec<T, 4>(&sh.b[t][n], fb);
-          load_vec<T, 4>(&sh.c[t][n], fc);
-          if (n + 4 > d.N)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (n + k >= d.N) fb[k] = fc[k] = 0.f;
-        }
-        store_vec<float, 4>(&sh.B[t][n], fb);
-        store_vec<float, 4>(&sh.C[t][n], fc);
-      }
+      convert(buf);
       __syncthreads();
-      if (!last) {
-        fetch(row, t0 + S::kSteps, steps_of(len, t0 + S::kSteps));
-      } else if (row + 1 < row1) {
-        fetch(row + 1, 0, steps_of(next_len, 0));
-        load_state(row + 1, next);
-      }
-
-      const int s0 = wt * kChunk;  // the warp's first step in the tile
-      float2 decay[kChunk][2];
-      if constexpr (WT > 1) {
-        float2 l[2] = {two(0.f), two(0.f)};
-        float sum = 0.f;
+      const bool last = t + kTile >= end;
+      if (!last)
+        fetch(row, t + kTile, end, buf ^ 1);
+      else if (more)
+        fetch(row + 1, tb, next_end, buf ^ 1);
+      if (!LOCAL && a.checkpoints && on)
+        store_pairs<S>(a.checkpoints + ((row * d.chunks + t / kChunk) * d.D + c) * d.N, n0, d.N, wide, h);
+#pragma unroll 1
+      for (int s = 0; s < kTile && t + s < end; s += kAhead) {
+        const int n = end - t - s;  // steps left
+        float du[kAhead], dd[kAhead], dz[kAhead];
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-          const float2 dx = sh.dx[s0 + j][ch];
-          const float4 b = *reinterpret_cast<const float4*>(&sh.B[s0 + j][n0]);
-          decay[j][0] = exp2_2(__fmul2_rn(two(dx.x), A2[0]));
-          decay[j][1] = exp2_2(__fmul2_rn(two(dx.x), A2[1]));
-          l[0] = __ffma2_rn(decay[j][0], l[0], __fmul2_rn(two(dx.y), make_float2(b.x, b.y)));
-          l[1] = __ffma2_rn(decay[j][1], l[1], __fmul2_rn(two(dx.y), make_float2(b.z, b.w)));
-          sum += dx.x;
+        for (int j = 0; j < kAhead; ++j) {
+          du[j] = to_f(ru[j]);
+          dd[j] = to_f(rd[j]);
+          dz[j] = gate ? to_f(rz[j]) : 0.f;
         }
-        if (wt < WT - 1) {
-          const float2 p0 = exp2_2(__fmul2_rn(two(sum), A2[0])), p1 = exp2_2(__fmul2_rn(two(sum), A2[1]));
-          *reinterpret_cast<float4*>(&sh.decay[wt][ch][n0]) = make_float4(p0.x, p0.y, p1.x, p1.y);
-          *reinterpret_cast<float4*>(&sh.state[wt][ch][n0]) = make_float4(l[0].x, l[0].y, l[1].x, l[1].y);
+        if (n > kAhead) {
+          load(n - kAhead);
+        } else if (more) {
+          at(row + 1);
+          load(next_end - tb);
         }
-        if (t0 > 0) {  // where the tile before ended; written again only after the barrier
-          const float4 e = *reinterpret_cast<const float4*>(&sh.end[ch][n0]);
-          h[0] = make_float2(e.x, e.y);
-          h[1] = make_float2(e.z, e.w);
-        }
-        __syncthreads();
-        for (int w = 0; w < wt; ++w) {
-          const float4 p = *reinterpret_cast<const float4*>(&sh.decay[w][ch][n0]);
-          const float4 e = *reinterpret_cast<const float4*>(&sh.state[w][ch][n0]);
-          h[0] = __ffma2_rn(make_float2(p.x, p.y), h[0], make_float2(e.x, e.y));
-          h[1] = __ffma2_rn(make_float2(p.z, p.w), h[1], make_float2(e.z, e.w));
-        }
-      }
-      if (a.checkpoints && on && s0 < steps) {
-        float* k = a.checkpoints + ((row * d.chunks + t0 / kChunk + wt) * d.D + c0 + ch) * d.N;
-        store_states(k, n0, d.N, h);
-      }
-      constexpr int U = steps_per_sum<LN>();
-      T* o = out + (t0 + s0 + q % U) * a.out.step + ch;
+        auto run = [&](auto all) {  // the steps; all: kAhead of them, with no checks in between
+          constexpr bool whole = decltype(all)::value;
 #pragma unroll
-      for (int j0 = 0; j0 < kChunk; j0 += U) {
-        float y[U];
+          for (int j = 0; j < kAhead; j += 2) {
+            if (!whole && j >= n) break;
+            float2 dt = __fadd2_rn(make_float2(dd[j], dd[j + 1]), two(bias));
+            if (softplus) dt = softplus_2(dt);
+            if (!whole && j + 1 >= n) dt.y = 0.f;
+            const float2 u = make_float2(du[j], whole || j + 1 < n ? du[j + 1] : 0.f);
+            const float2 x = __fmul2_rn(dt, u);
+            const float2 gz = gate ? silu_2(make_float2(dz[j], dz[j + 1])) : two(1.f);
+            if (LOCAL) sum += dt.x + dt.y;
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const float2 dx = sh.dx[s0 + j0 + j][ch];
-          const float4 b = *reinterpret_cast<const float4*>(&sh.B[s0 + j0 + j][n0]);
-          const float4 c = *reinterpret_cast<const float4*>(&sh.C[s0 + j0 + j][n0]);
-          if constexpr (WT == 1) {
-            decay[j0 + j][0] = exp2_2(__fmul2_rn(two(dx.x), A2[0]));
-            decay[j0 + j][1] = exp2_2(__fmul2_rn(two(dx.x), A2[1]));
+            for (int e = 0; e < 2; ++e) {
+              if (!whole && e == 1 && j + 1 >= n) break;
+              const float2 d1 = two(e ? dt.y : dt.x), x1 = two(e ? x.y : x.x);
+              const float4* B = reinterpret_cast<const float4*>(&sh.f[buf][0][s + j + e][n0]);
+              const float4* C = reinterpret_cast<const float4*>(&sh.f[buf][1][s + j + e][n0]);
+              float2 y = two(0.f);
+#pragma unroll
+              for (int i = 0; i < H; i += 2) {
+                const float4 b = B[i / 2];
+                h[i] = __ffma2_rn(exp2_2(__fmul2_rn(d1, A2[i])), h[i], __fmul2_rn(x1, make_float2(b.x, b.y)));
+                h[i + 1] = __ffma2_rn(exp2_2(__fmul2_rn(d1, A2[i + 1])), h[i + 1], __fmul2_rn(x1, make_float2(b.z, b.w)));
+                if (!LOCAL) {
+                  const float4 v = C[i / 2];
+                  y = __ffma2_rn(make_float2(v.x, v.y), h[i], y);
+                  y = __ffma2_rn(make_float2(v.z, v.w), h[i + 1], y);
+                }
+              }
+              if (!LOCAL) {
+                float v = y.x + y.y;
+#pragma unroll
+                for (int m = W; m < 32; m *= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+                v = fmaf(skip, e ? u.y : u.x, v) * (e ? gz.y : gz.x);
+                if (on && q == 0) out[(j + e) * a.out.step] = from_f<T>(v);
+              }
+            }
           }
-          h[0] = __ffma2_rn(decay[j0 + j][0], h[0], __fmul2_rn(two(dx.y), make_float2(b.x, b.y)));
-          h[1] = __ffma2_rn(decay[j0 + j][1], h[1], __fmul2_rn(two(dx.y), make_float2(b.z, b.w)));
-          const float2 e = __ffma2_rn(make_float2(c.z, c.w), h[1], __fmul2_rn(make_float2(c.x, c.y), h[0]));
-          y[j] = e.x + e.y;
-        }
-        const float v = sum_steps<LN>(y, q);
-        const int t = s0 + j0 + q % U;
-        if (q < U && on && t < steps) {
-          const float2 e = sh.out[t][ch];
-          *o = from_f<T>(t < valid ? (v + e.x) * e.y : 0.f);
-        }
-        o += U * a.out.step;
-        if (s0 + j0 + U >= steps) break;
+        };
+        if (n >= kAhead)
+          run(std::true_type());
+        else
+          run(std::false_type());
+        out += kAhead * a.out.step;
       }
-      if (WT > 1 && wt == WT - 1)
-        *reinterpret_cast<float4*>(&sh.end[ch][n0]) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+      buf ^= 1;
     }
-    if (a.state_out.ptr && on && wt == WT - 1)
-      store_states(a.state_out.ptr + row * a.state_out.stride + (c0 + ch) * d.N, n0, d.N, h);
-    len = next_len;
+    if (LOCAL) {
+      if (on) {
+        const int64_t at = ((int64_t)row * parts.n + part) * d.D + c;
+        store_pairs<S>(parts.state + at * d.N, n0, d.N, wide, h);
+        if (q == 0) parts.sum[at] = sum;
+      }
+    } else {
+      if (on && end < te) {  // behind the row's end: zeros, and the state as it is
+        const int from = end > tb ? end : tb;
+        if (q == 0)
+          for (int i = from; i < te; ++i)
+            static_cast<T*>(a.out.ptr)[row * a.out.row + i * a.out.step + c] = from_f<T>(0.f);
+        if (a.checkpoints)
+          for (int i = (from + kChunk - 1) / kChunk; i * kChunk < te; ++i)
+            store_pairs<S>(a.checkpoints + ((row * d.chunks + i) * d.D + c) * d.N, n0, d.N, wide, h);
+      }
+      if (a.state_out.ptr && on && te == d.T)
+        store_pairs<S>(a.state_out.ptr + row * a.state_out.stride + c * d.N, n0, d.N, wide, h);
+      if (end <= tb && more) {  // nothing was computed that would have fetched this
+        at(row + 1);
+        load(next_end - tb);
+        __syncthreads();
+        fetch(row + 1, tb, next_end, buf);
+      }
+    }
+    end = next_end;
+  }
+}
+
+// state[row][k] becomes the state that part k starts from.
+__global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims d, Parts parts) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, DN = (int64_t)d.D * d.N;
+  if (i >= a.rows * DN) return;
+  const int64_t row = i / DN, cn = i % DN, c = cn / d.N, set = row / d.rows_per_set;
+  const float A2 = a.A.ptr[set * a.A.stride + cn] * kLog2e;
+  float h = a.state_in.ptr ? a.state_in.ptr[row * a.state_in.stride + cn] : 0.f;
+  for (int k = 0; k < parts.n; ++k) {
+    const int64_t at = row * parts.n + k;
+    float l = 0.f, s = 0.f;
+    if (k + 1 < parts.n) {
+      l = parts.state[at * DN + cn];
+      s = parts.sum[at * d.D + c];
+    }
+    parts.state[at * DN + cn] = h;
+    h = fmaf(exp2_1(s * A2), h, l);
   }
 }
 
@@ -706,40 +695,79 @@ int copy_bytes(std::initializer_list<const zo_tensor*> tensors, int elem, int64_
   return bytes < 4 ? 0 : bytes;
 }
 
-template <class T, int LN, int WT, int WC>
-cudaError_t run_scan_tiled(const zo_scan_args& a, cudaStream_t st) {
-  using S = Tile<T, LN, WT, WC>;
-  ScanDims d = scan_dims<LN>(a);
-  d.tiles = (int)ceil_div(d.Dg, S::kChannels);
-  // Rows that fit one tile go several to a block, as long as that leaves 16
-  // blocks an SM: the block's first loads are waited for once for all of them.
-  int64_t rows = 1;
-  if (a.seq <= S::kSteps) rows = (int64_t)d.tiles * d.G * a.rows / (16 * kBlockSMs);
-  rows = rows < 1 ? 1 : rows > d.rows_per_set ? d.rows_per_set : rows;
-  const int64_t blocks = (int64_t)d.tiles * d.G * ceil_div(d.rows_per_set, rows) * a.sets;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  constexpr int kRow = S::kChannels * (int)sizeof(T);
-  int copy = copy_bytes({&a.u, &a.delta, &a.z}, sizeof(T), d.Dg);
-  if (copy > kRow) copy = kRow;
-  const int copy_bc = copy_bytes({&a.B, &a.C}, sizeof(T), d.N);
-  const cudaError_t e = cudaFuncSetAttribute(
-      scan_kernel<T, LN, WT, WC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(S));
-  if (e != cudaSuccess) return e;
-  scan_kernel<T, LN, WT, WC>
-      <<<(unsigned)blocks, S::kThreads, sizeof(S), st>>>(a, d, (int)rows, copy, copy_bc);
-  count_launch();
-  return cudaGetLastError();
+// States a lane and lanes a channel.
+int states_per_lane(int N) { return N <= 4 ? 4 : N <= 8 ? 8 : 16; }
+int lanes_per_channel(int N) {
+  int n = 1;
+  while (n * states_per_lane(N) < N) n *= 2;
+  return n;
 }
 
-// Rows of at most two chunks are walked by one warp a channel group; longer ones
-// by several along time (eight where a warp's channels still fill sectors).
-template <class T, int LN>
-cudaError_t run_scan(const zo_scan_args& a, cudaStream_t st) {
-  if (a.seq <= 2 * kChunk) return run_scan_tiled<T, LN, 1, 4>(a, st);
-  if constexpr (LN <= 4)
-    return run_scan_tiled<T, LN, 8, 1>(a, st);
-  else
-    return run_scan_tiled<T, LN, 4, 2>(a, st);
+// Warps of a block (at most four, and no more than a group's channels fill),
+// and the parts of time.  One pass over time with w warps a scheduler (592 of
+// them) runs at about min(w, 1) of the special function unit's rate; in parts the
+// exponentials come twice (37 instead of 21 results a value).  So time is divided
+// where there are under half as many warps as schedulers, into as many parts as
+// make four blocks an SM at most (which is what stays there), of 64 steps at least.
+struct ScanPlan {
+  int warps, tiles, parts, steps;
+};
+ScanPlan scan_plan(const zo_scan_args& a) {
+  ScanPlan p;
+  const int64_t Dg = a.channels / a.groups, per_warp = 32 / lanes_per_channel(a.states);
+  const int64_t w = ceil_div(Dg, per_warp);
+  p.warps = w < 4 ? (int)w : 4;
+  p.tiles = (int)ceil_div(w, p.warps);
+  const int64_t all = w * a.groups * a.rows;
+  const int64_t blocks = (int64_t)p.tiles * a.groups * a.rows;
+  int64_t n = all * 2 < 4 * kBlockSMs ? 4 * kBlockSMs / blocks : 1;
+  int64_t steps = ceil_div(ceil_div(a.seq, n), kChunk) * kChunk;
+  if (n > 1 && steps < 64) steps = 64;
+  p.parts = (int)ceil_div(a.seq, steps);
+  p.steps = p.parts > 1 ? (int)steps : (int)(ceil_div(a.seq, kChunk) * kChunk);
+  return p;
+}
+
+template <class T, int S, int LN>
+cudaError_t run_scan(const zo_scan_args& a, float* ws, cudaStream_t st) {
+  const ScanPlan plan = scan_plan(a);
+  ScanDims d = scan_dims<LN>(a);
+  d.tiles = plan.tiles;
+  const int64_t DN = (int64_t)d.D * d.N;
+  const Parts parts{plan.parts, plan.steps, ws, ws + (int64_t)a.rows * plan.parts * DN};
+  // Short rows go several to a block, as long as that leaves 16 blocks an SM: A
+  // and the block's first loads are waited for once for all of them.
+  const int64_t per_row = (int64_t)d.tiles * d.G;
+  int64_t rows = plan.parts == 1 && a.seq <= 4 * kTile ? per_row * a.rows / (16 * kBlockSMs) : 1;
+  rows = rows < 1 ? 1 : rows > d.rows_per_set ? d.rows_per_set : rows;
+  const int64_t row_blocks = ceil_div(d.rows_per_set, rows) * a.sets;
+  const int64_t blocks = per_row * row_blocks * plan.parts;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int copy = copy_bytes({&a.B, &a.C}, sizeof(T), d.N);
+  bool wide = d.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.checkpoints) % 16 == 0;
+  for (const zo_f32* p : {&a.state_in, &a.state_out})
+    wide = wide && p->stride % 4 == 0 && reinterpret_cast<uintptr_t>(p->ptr) % 16 == 0;
+  const int threads = 32 * plan.warps;
+  constexpr int kSmem = (int)sizeof(BC<T, S * LN>);
+  cudaError_t e = cudaSuccess;
+  if (plan.parts > 1) {
+    if ((e = cudaFuncSetAttribute(scan_kernel<T, S, LN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  kSmem)) != cudaSuccess)
+      return e;
+    scan_kernel<T, S, LN, true><<<(unsigned)(per_row * row_blocks * (plan.parts - 1)), threads, kSmem, st>>>(
+        a, d, parts, (int)rows, copy, d.N % 4 == 0);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    scan_join_kernel<<<(unsigned)ceil_div(a.rows * DN, 256), 256, 0, st>>>(a, d, parts);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if ((e = cudaFuncSetAttribute(scan_kernel<T, S, LN, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmem)) != cudaSuccess)
+    return e;
+  scan_kernel<T, S, LN, false><<<(unsigned)blocks, threads, kSmem, st>>>(a, d, parts, (int)rows, copy, wide);
+  count_launch();
+  return cudaGetLastError();
 }
 
 template <class T, int LN, int RG>
@@ -808,6 +836,20 @@ auto by_lanes(int states, F&& f) {
 }
 
 template <class F>
+cudaError_t by_states(int states, F&& f) {
+  using std::integral_constant;
+  switch (lanes_per_channel(states)) {
+    case 1:
+      return states <= 4   ? f(integral_constant<int, 4>(), integral_constant<int, 1>())
+             : states <= 8 ? f(integral_constant<int, 8>(), integral_constant<int, 1>())
+                           : f(integral_constant<int, 16>(), integral_constant<int, 1>());
+    case 2: return f(integral_constant<int, 16>(), integral_constant<int, 2>());
+    case 4: return f(integral_constant<int, 16>(), integral_constant<int, 4>());
+    default: return f(integral_constant<int, 16>(), integral_constant<int, 8>());
+  }
+}
+
+template <class F>
 cudaError_t by_type(int dtype, F&& f) {
   switch (dtype) {
     case ZO_DTYPE_BF16: return f(__nv_bfloat16());
@@ -818,7 +860,10 @@ cudaError_t by_type(int dtype, F&& f) {
 
 }  // namespace
 
-int64_t scan_workspace(const zo_scan_args&) { return 0; }
+int64_t scan_workspace(const zo_scan_args& a) {
+  const ScanPlan p = scan_plan(a);
+  return p.parts == 1 ? 0 : (int64_t)a.rows * p.parts * a.channels * (a.states + 1) * (int64_t)sizeof(float);
+}
 
 int64_t scan_backward_workspace(const zo_scan_args& a) {
   return by_lanes(a.states, [&](auto ln) {
@@ -828,10 +873,10 @@ int64_t scan_backward_workspace(const zo_scan_args& a) {
   });
 }
 
-cudaError_t launch_scan(const zo_scan_args& a, float*, cudaStream_t st) {
+cudaError_t launch_scan(const zo_scan_args& a, float* ws, cudaStream_t st) {
   return by_type(a.dtype, [&](auto t) {
-    return by_lanes(a.states, [&](auto ln) {
-      return run_scan<decltype(t), decltype(ln)::value>(a, st);
+    return by_states(a.states, [&](auto s, auto ln) {
+      return run_scan<decltype(t), decltype(s)::value, decltype(ln)::value>(a, ws, st);
     });
   });
 }
