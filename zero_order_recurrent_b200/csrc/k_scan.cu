@@ -517,143 +517,498 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, Sca
 }
 
 // ---- backward ------------------------------------------------------------------
-
-// Backwards through time, chunk by chunk: the states of a chunk are run again
-// from its checkpoint, then g_t = C_t dy_t + a_{t+1} g_{t+1} comes back through
-// it.  With a_t h_{t-1} = w:
+//
+// With a_t h_{t-1} = w_t and g_t = C_t dy_t + a_{t+1} g_{t+1}, dy = dout silu(z):
 //   dC_t = sum_c dy h;  dB_t = sum_c g d u;  du = d sum_n g B + skip dy
 //   dd = sum_n g (A w + u B);  ddelta = dd softplus'(raw);  dA = sum_t g w d
+//   dskip = sum_t dy u;  dbias = sum_t ddelta;  dz = dout y silu'(z)
+
+// The lanes' sums of NV values: lane l gets, in v[0 ..], those of the values whose index has
+// the bits of l / STRIDE on top (lowest bit first); where lanes outnumber values, several
+// lanes get the same.
+template <int NV, int LANES, int STRIDE>
+__device__ __forceinline__ void sum_over(float* v, int lane) {
+  if constexpr (LANES > 1) {
+    if constexpr (NV > 1) {
+      const bool up = lane & STRIDE;
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i) {
+        const float keep = up ? v[i + NV / 2] : v[i], give = up ? v[i] : v[i + NV / 2];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, STRIDE);
+      }
+      sum_over<NV / 2, LANES / 2, STRIDE * 2>(v, lane);
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], STRIDE);
+      sum_over<1, LANES / 2, STRIDE * 2>(v, lane);
+    }
+  }
+}
+
+// The same for three values of each of four channels, over LN lanes: lane q gets, in v[0 ..],
+// the three of channel 2 (q & 1) + (q >> 1 & 1) (of two or four channels where LN is 2 or 1).
+template <int LN>
+__device__ __forceinline__ void sum_over12(float* v, int lane) {
+  if constexpr (LN >= 2) sum_over<12, 2, 1>(v, lane);
+  if constexpr (LN >= 4) sum_over<6, 2, 2>(v, lane);
+  if constexpr (LN >= 8)
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int m = 4; m < LN; m *= 2) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
+}
+
+// A lane's carry over one part of time from the carry 0 at its end:
+// carry <- a_t (carry + C_t dy_t), t backwards; parts 1 .. n-1, into parts.state and sum.
+template <class T, int S, int LN>
+__global__ void __launch_bounds__(128, 4)
+    scan_carry_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, Parts parts) {
+  constexpr int NP = S * LN, W = 32 / LN, H = S / 2;
+  __shared__ __align__(16) float C[kTile][NP];
+  const unsigned tiles = d.tiles * d.G;
+  const unsigned tile_g = blockIdx.x % tiles, rest = blockIdx.x / tiles;
+  const int part = 1 + rest % (parts.n - 1), row = rest / (parts.n - 1);
+  const int tile = tile_g % d.tiles, grp = tile_g / d.tiles, set = row / d.rows_per_set;
+  const int tb = part * parts.steps, te = tb + parts.steps < d.T ? tb + parts.steps : (int)d.T;
+  const int lane = threadIdx.x % 32, q = lane / W, n0 = q * S;
+  const int k = (tile * (int)(blockDim.x / 32) + (int)threadIdx.x / 32) * W + lane % W;
+  const bool on = k < d.Dg;
+  const int64_t c = (int64_t)grp * d.Dg + (on ? k : 0);
+  float2 A2[H], v[H];
+  load_pairs<S>(a.A.ptr + set * a.A.stride + c * d.N, n0, d.N, false, A2);
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    A2[i] = __fmul2_rn(A2[i], two(kLog2e));
+    v[i] = two(0.f);
+  }
+  const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[set * a.delta_bias.stride + c] : 0.f;
+  const bool softplus = a.flags & ZO_SCAN_SOFTPLUS, gate = a.z.ptr;
+  const int len = (int)row_length(a.lengths, row, d.T, nullptr, false), end = len < te ? len : te;
+  const T* pd = static_cast<const T*>(a.delta.ptr) + row * a.delta.row + c;
+  const T* pz = static_cast<const T*>(a.z.ptr) + (gate ? row * a.z.row + c : 0);
+  const T* po = static_cast<const T*>(g.dout.ptr) + row * g.dout.row + c;
+  const T* pc = static_cast<const T*>(a.C.ptr) + row * a.C.row + (int64_t)grp * d.N;
+  float sum = 0.f;
+  for (int t = tb + (end > tb ? (end - 1 - tb) / kTile * kTile : -kTile); t >= tb; t -= kTile) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTile * NP; i += blockDim.x) {
+      const int s = i / NP, n = i % NP;
+      C[s][n] = t + s < end && n < d.N ? to_f(pc[(t + s) * a.C.step + n]) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int s = kTile - 4; s >= 0; s -= 4) {
+      float2 dt[2], dy[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float rd[2], ro[2], rz[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t u = t + s + 2 * j + e;
+          const bool in = u < end;
+          rd[e] = in ? to_f(pd[u * a.delta.step]) : 0.f;
+          ro[e] = in ? to_f(po[u * g.dout.step]) : 0.f;
+          rz[e] = in && gate ? to_f(pz[u * a.z.step]) : 0.f;
+        }
+        dt[j] = __fadd2_rn(make_float2(rd[0], rd[1]), two(bias));
+        if (softplus) dt[j] = softplus_2(dt[j]);
+        if (t + s + 2 * j >= end) dt[j].x = 0.f;
+        if (t + s + 2 * j + 1 >= end) dt[j].y = 0.f;
+        dy[j] = make_float2(ro[0], ro[1]);
+        if (gate) dy[j] = __fmul2_rn(dy[j], silu_2(make_float2(rz[0], rz[1])));
+        sum += dt[j].x + dt[j].y;
+      }
+#pragma unroll
+      for (int j = 3; j >= 0; --j) {
+        const float2 d1 = two(j % 2 ? dt[j / 2].y : dt[j / 2].x), y1 = two(j % 2 ? dy[j / 2].y : dy[j / 2].x);
+        const float4* cs = reinterpret_cast<const float4*>(&C[s + j][n0]);
+#pragma unroll
+        for (int i = 0; i < H; i += 2) {
+          const float4 f = cs[i / 2];
+          v[i] = __fmul2_rn(exp2_2(__fmul2_rn(d1, A2[i])), __ffma2_rn(y1, make_float2(f.x, f.y), v[i]));
+          v[i + 1] = __fmul2_rn(exp2_2(__fmul2_rn(d1, A2[i + 1])), __ffma2_rn(y1, make_float2(f.z, f.w), v[i + 1]));
+        }
+      }
+    }
+  }
+  if (on) {
+    const int64_t at = ((int64_t)row * parts.n + part) * d.D + c;
+    store_pairs<S>(parts.state + at * d.N, n0, d.N, d.N % 4 == 0, v);
+    if (q == 0) parts.sum[at] = sum;
+  }
+}
+
+// state[row][k] becomes the carry that comes into part k at its end.
+__global__ void __launch_bounds__(256) carry_join_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, Parts parts) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, DN = (int64_t)d.D * d.N;
+  if (i >= a.rows * DN) return;
+  const int64_t row = i / DN, cn = i % DN, c = cn / d.N, set = row / d.rows_per_set;
+  const float A2 = a.A.ptr[set * a.A.stride + cn] * kLog2e;
+  float v = g.dstate_out.ptr ? g.dstate_out.ptr[row * g.dstate_out.stride + cn] : 0.f;
+  for (int k = parts.n - 1; k >= 0; --k) {
+    const int64_t at = row * parts.n + k;
+    float l = 0.f, s = 0.f;
+    if (k > 0) {
+      l = parts.state[at * DN + cn];
+      s = parts.sum[at * d.D + c];
+    }
+    parts.state[at * DN + cn] = v;
+    v = fmaf(exp2_1(s * A2), v, l);
+  }
+}
+
+constexpr int kSub = 2;      // steps whose states and decays are in registers together
+constexpr int kFlush = 64;   // chunks after which the parameters' sums are put away
+
+template <int LN>
+struct BackTile {
+  static constexpr int kWarps = LN >= 4 ? 4 : LN;          // 128 channels a block, or less
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kWarpChannels = 128 / LN, kChannels = kWarps * kWarpChannels;
+  static constexpr int NP = 4 * LN, kMid = kChunk / kSub - 1;
+  alignas(16) float d[kChunk][kChannels], u[kChunk][kChannels], dy[kChunk][kChannels];
+  float slope[kChunk][kChannels], zf[kChunk][kChannels];   // softplus'(raw), dout silu'(z)
+  alignas(16) float B[kChunk][NP], C[kChunk][NP];
+  alignas(16) float4 mid[kMid][4][kThreads];               // the states before the later sub-blocks
+  float bc[kWarps][kChunk][2 * NP];                        // the warps' sums for dB and dC
+};
+
+// What the backward pass leaves to be summed up: dB and dC by channel tile, the parameters'
+// gradients by row, part and flush.
+struct BackSums {
+  float *bc, *A, *skip, *bias;
+  int flushes;  // of a row's part
+};
+
+// A lane holds 4 neighbouring channels x 4 states, in pairs of channels: so the sums
+// over a channel's states (12 values: two for the gradients, one for y) and those over
+// channels (8 values: dB, dC) are both half done in the lane, and take 16 shuffles a step
+// and warp where 16 states a lane would take 31 and 4 states of one channel a lane 37.
+//
+// Chunk by chunk backwards: the states are run forward from the chunk's checkpoint,
+// keeping those before each kSub steps in shared memory; then, backwards over those
+// sub-blocks, states and decays are run again into registers and the carry comes back
+// through them.  The exponentials are so done nearly twice, which is less than to
+// keep every state in memory.
+//
+// Bound: by count the special function unit (37 of its results for a value with 16
+// states), the multiply-add pipe and issue are about equal.
 template <class T, int LN>
-__global__ void __launch_bounds__(kThreads)
-    scan_backward_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, float* part_bc, float* part_a,
-                         float* part_skip, float* part_bias) {
-  extern __shared__ float sh[];  // [warp][step][dB, dC][4 LN]
-  const Place p = place<LN>(d, blockIdx.x);
-  const int64_t len = row_length(a.lengths, p.row, d.T, a.status, p.tile == 0 && threadIdx.x == 0);
-  const int lane = (int)threadIdx.x % LN, warp = (int)threadIdx.x / 32;
-  const int64_t cn = (int64_t)p.c * d.N;
-  float A[4], gr[4], dA[4] = {0.f, 0.f, 0.f, 0.f}, ds = 0.f, db = 0.f;
-  load_states(a.A.ptr + p.set * a.A.stride + cn, p.n0, d.N, A);
-  if (g.dstate_out.ptr)
-    load_states(g.dstate_out.ptr + p.row * g.dstate_out.stride + cn, p.n0, d.N, gr);
+__global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / LN / 2)
+    scan_backward_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, Parts parts, BackSums sums, bool vec) {
+  using S = BackTile<LN>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  S& sh = *reinterpret_cast<S*>(smem);
+  const unsigned tiles = d.tiles * d.G;
+  const unsigned tile_g = blockIdx.x % tiles, rest = blockIdx.x / tiles;
+  const int part = rest % parts.n, row = rest / parts.n;
+  const int tile = tile_g % d.tiles, grp = tile_g / d.tiles, set = row / d.rows_per_set;
+  const int tb = part * parts.steps, te = tb + parts.steps < d.T ? tb + parts.steps : (int)d.T;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, q = lane % LN, n0 = 4 * q;
+  const int ch = warp * S::kWarpChannels + lane / LN * 4;  // the lane's first channel in the tile
+  const int left = d.Dg - tile * S::kChannels;             // channels of the group from the tile on
+  const int64_t c0 = (int64_t)grp * d.Dg + tile * S::kChannels;
+  const bool softplus = a.flags & ZO_SCAN_SOFTPLUS, gate = a.z.ptr;
+  const int len = (int)row_length(a.lengths, row, d.T, a.status, tile == 0 && part == 0 && tid == 0);
+  const int end = len < te ? len : te;
+
+  // [state][pair of channels]
+  float2 A2[4][2], gr[4][2], dA[4][2];
+  auto load_lane = [&](const float* p, float2 (&f)[4][2]) {  // [channel][N] from the tile's first channel
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (ch + i < left) {
+        const float* s = p + (int64_t)(ch + i) * d.N;
+        if (d.N % 4 == 0 && reinterpret_cast<uintptr_t>(s) % 16 == 0)
+          load_states4<true>(s, n0, d.N, v);
+        else
+          load_states4<false>(s, n0, d.N, v);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) (i % 2 ? f[n][i / 2].y : f[n][i / 2].x) = v[n];
+    }
+  };
+  auto store_lane = [&](float* p, const float2 (&f)[4][2]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (ch + i < left) {
+        float v[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) v[n] = i % 2 ? f[n][i / 2].y : f[n][i / 2].x;
+        store_states4<false>(p + (int64_t)(ch + i) * d.N, n0, d.N, v);
+      }
+  };
+  load_lane(a.A.ptr + set * a.A.stride + c0 * d.N, A2);
+  if (parts.n > 1)
+    load_lane(parts.state + (((int64_t)row * parts.n + part) * d.D + c0) * d.N, gr);
+  else if (g.dstate_out.ptr)
+    load_lane(g.dstate_out.ptr + row * g.dstate_out.stride + c0 * d.N, gr);
   else
-    gr[0] = gr[1] = gr[2] = gr[3] = 0.f;
-  const float skip = a.skip.ptr ? a.skip.ptr[p.set * a.skip.stride + p.c] : 0.f;
-  const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[p.set * a.delta_bias.stride + p.c] : 0.f;
-  const T* u = static_cast<const T*>(a.u.ptr) + p.row * a.u.row + p.c;
-  const T* dl = static_cast<const T*>(a.delta.ptr) + p.row * a.delta.row + p.c;
-  const T* z = a.z.ptr ? static_cast<const T*>(a.z.ptr) + p.row * a.z.row + p.c : nullptr;
-  const T* B = static_cast<const T*>(a.B.ptr) + p.row * a.B.row + (int64_t)p.g * d.N;
-  const T* C = static_cast<const T*>(a.C.ptr) + p.row * a.C.row + (int64_t)p.g * d.N;
-  const T* dout = static_cast<const T*>(g.dout.ptr) + p.row * g.dout.row + p.c;
-  T* du = static_cast<T*>(g.du.ptr) + p.row * g.du.row + p.c;
-  T* dd = static_cast<T*>(g.ddelta.ptr) + p.row * g.ddelta.row + p.c;
-  T* dz = z ? static_cast<T*>(g.dz.ptr) + p.row * g.dz.row + p.c : nullptr;
-  for (int64_t k = d.chunks - 1; k >= 0; --k) {
-    const int64_t t0 = k * kChunk;
-    float h[kChunk + 1][4];
-    load_states(a.checkpoints + (p.row * d.chunks + k) * d.D * d.N + cn, p.n0, d.N, h[0]);
-    for (int j = 0; j < kChunk; ++j) {
-      const int64_t t = t0 + j;
-      if (t < len) {
-        const float raw = to_f(dl[t * a.delta.step]) + bias;
-        const float dt = a.flags & ZO_SCAN_SOFTPLUS ? softplus_f(raw) : raw;
-        const float x = dt * to_f(u[t * a.u.step]);
-        float Bt[4];
-        load_states(B + t * a.B.step, p.n0, d.N, Bt);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[j + 1][i] = fmaf(expf(dt * A[i]), h[j][i], x * Bt[i]);
+    for (int n = 0; n < 4; ++n) gr[n][0] = gr[n][1] = two(0.f);
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      A2[n][p] = __fmul2_rn(A2[n][p], two(kLog2e));
+      dA[n][p] = two(0.f);
+    }
+
+  // After the sums over states a lane has MC of its four channels, from `mine` on.
+  constexpr int MC = LN >= 4 ? 1 : 4 / LN;
+  const int mine = ch + (LN == 1 ? 0 : LN == 2 ? 2 * (q & 1) : 2 * (q & 1) + (q >> 1 & 1));
+  float skip[MC], ds[MC], db[MC];
+#pragma unroll
+  for (int i = 0; i < MC; ++i) {
+    skip[i] = a.skip.ptr && mine + i < left ? a.skip.ptr[set * a.skip.stride + c0 + mine + i] : 0.f;
+    ds[i] = db[i] = 0.f;
+  }
+  const bool writes = LN < 4 || q < 4;
+  T* pdu = static_cast<T*>(g.du.ptr) + row * g.du.row + c0 + mine;
+  T* pdd = static_cast<T*>(g.ddelta.ptr) + row * g.ddelta.row + c0 + mine;
+  T* pdz = static_cast<T*>(g.dz.ptr) + (gate ? row * g.dz.row + c0 + mine : 0);
+
+  // behind the row's end
+  if (writes)
+    for (int t = end > tb ? end : tb; t < te; ++t)
+#pragma unroll
+      for (int i = 0; i < MC; ++i)
+        if (mine + i < left) {
+          pdu[t * g.du.step + i] = from_f<T>(0.f);
+          pdd[t * g.ddelta.step + i] = from_f<T>(0.f);
+          if (gate) pdz[t * g.dz.step + i] = from_f<T>(0.f);
+        }
+
+  int flush = 0;
+  auto put_away = [&] {  // the parameters' sums so far
+    const int64_t at = ((int64_t)row * parts.n + part) * sums.flushes + flush++;
+    store_lane(sums.A + (at * d.D + c0) * d.N, dA);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) dA[n][0] = dA[n][1] = two(0.f);
+#pragma unroll
+    for (int i = 0; i < MC; ++i) {
+      if (writes && mine + i < left) {
+        sums.skip[at * d.D + c0 + mine + i] = ds[i];
+        sums.bias[at * d.D + c0 + mine + i] = db[i];
+      }
+      ds[i] = db[i] = 0.f;
+    }
+  };
+
+  const T* bu = static_cast<const T*>(a.u.ptr) + row * a.u.row + c0;
+  const T* bd = static_cast<const T*>(a.delta.ptr) + row * a.delta.row + c0;
+  const T* bz = static_cast<const T*>(a.z.ptr) + (gate ? row * a.z.row + c0 : 0);
+  const T* bo = static_cast<const T*>(g.dout.ptr) + row * g.dout.row + c0;
+  const T* bB = static_cast<const T*>(a.B.ptr) + row * a.B.row + (int64_t)grp * d.N;
+  const T* bC = static_cast<const T*>(a.C.ptr) + row * a.C.row + (int64_t)grp * d.N;
+
+  int chunks = 0;
+  for (int t0 = end > tb ? tb + (end - 1 - tb) / kChunk * kChunk : tb - 1; t0 >= tb; t0 -= kChunk) {
+    __syncthreads();
+    // The chunk's inputs and what is one channel's and step's, four channels at a time.
+#pragma unroll 2
+    for (int i = tid; i < kChunk * S::kChannels / 4; i += S::kThreads) {
+      const int s = i / (S::kChannels / 4), c = i % (S::kChannels / 4) * 4;
+      const int64_t t = t0 + s;
+      float fu[4] = {}, fd[4] = {}, fz[4] = {}, fo[4] = {};
+      if (t < end) {
+        if (vec && c < left) {
+          load_vec<T, 4>(bu + t * a.u.step + c, fu);
+          load_vec<T, 4>(bd + t * a.delta.step + c, fd);
+          load_vec<T, 4>(bo + t * g.dout.step + c, fo);
+          if (gate) load_vec<T, 4>(bz + t * a.z.step + c, fz);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < left) {
+              fu[e] = to_f(bu[t * a.u.step + c + e]);
+              fd[e] = to_f(bd[t * a.delta.step + c + e]);
+              fo[e] = to_f(bo[t * g.dout.step + c + e]);
+              if (gate) fz[e] = to_f(bz[t * a.z.step + c + e]);
+            }
+        }
+      }
+      float o[5][4];
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const float2 k = a.delta_bias.ptr ? make_float2(c + e < left ? a.delta_bias.ptr[set * a.delta_bias.stride + c0 + c + e] : 0.f,
+                                                        c + e + 1 < left ? a.delta_bias.ptr[set * a.delta_bias.stride + c0 + c + e + 1] : 0.f)
+                                          : two(0.f);
+        const float2 raw = __fadd2_rn(make_float2(fd[e], fd[e + 1]), k);
+        float2 dt = raw, slope = two(1.f), dy = make_float2(fo[e], fo[e + 1]), zf = two(0.f);
+        if (softplus) {
+          dt = softplus_2(raw);
+          slope = rcp_2(__fadd2_rn(exp2_2(__fmul2_rn(raw, two(-kLog2e))), two(1.f)));
+        }
+        if (gate) {
+          const float2 z = make_float2(fz[e], fz[e + 1]);
+          const float2 r = rcp_2(__fadd2_rn(exp2_2(__fmul2_rn(z, two(-kLog2e))), two(1.f)));
+          const float2 v = __fmul2_rn(z, r);  // silu
+          zf = __fmul2_rn(dy, __ffma2_rn(v, __ffma2_rn(r, two(-1.f), two(1.f)), r));
+          dy = __fmul2_rn(dy, v);
+        }
+        const bool in = t < end;
+        o[0][e] = in ? dt.x : 0.f, o[0][e + 1] = in ? dt.y : 0.f;
+        o[1][e] = fu[e], o[1][e + 1] = fu[e + 1];
+        o[2][e] = dy.x, o[2][e + 1] = dy.y;
+        o[3][e] = slope.x, o[3][e + 1] = slope.y;
+        o[4][e] = zf.x, o[4][e + 1] = zf.y;
+      }
+      store_vec<float, 4>(&sh.d[s][c], o[0]);
+      store_vec<float, 4>(&sh.u[s][c], o[1]);
+      store_vec<float, 4>(&sh.dy[s][c], o[2]);
+      store_vec<float, 4>(&sh.slope[s][c], o[3]);
+      store_vec<float, 4>(&sh.zf[s][c], o[4]);
+    }
+    for (int i = tid; i < kChunk * S::NP; i += S::kThreads) {
+      const int s = i / S::NP, n = i % S::NP;
+      const bool in = t0 + s < end && n < d.N;
+      sh.B[s][n] = in ? to_f(bB[(t0 + s) * a.B.step + n]) : 0.f;
+      sh.C[s][n] = in ? to_f(bC[(t0 + s) * a.C.step + n]) : 0.f;
+    }
+    float2 h0[4][2];
+    load_lane(a.checkpoints + ((row * d.chunks + t0 / kChunk) * d.D + c0) * d.N, h0);
+    __syncthreads();
+
+    auto step = [&](int s, float2 (&h)[4][2], float2 (&at)[4][2]) {
+      const float4 dt = *reinterpret_cast<const float4*>(&sh.d[s][ch]);
+      const float4 u = *reinterpret_cast<const float4*>(&sh.u[s][ch]);
+      const float4 b4 = *reinterpret_cast<const float4*>(&sh.B[s][n0]);
+      const float2 d2[2] = {make_float2(dt.x, dt.y), make_float2(dt.z, dt.w)};
+      const float2 x2[2] = {__fmul2_rn(d2[0], make_float2(u.x, u.y)), __fmul2_rn(d2[1], make_float2(u.z, u.w))};
+      const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          at[n][p] = exp2_2(__fmul2_rn(d2[p], A2[n][p]));
+          h[n][p] = __ffma2_rn(at[n][p], h[n][p], __fmul2_rn(x2[p], two(b[n])));
+        }
+    };
+    float2 hs[kSub + 1][4][2], at[kSub][4][2];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) hs[0][n][0] = h0[n][0], hs[0][n][1] = h0[n][1];
+    const int subs = (end - t0 < kChunk ? end - t0 + kSub - 1 : kChunk) / kSub;
+#pragma unroll 1
+    for (int m = 0; m + 1 < subs; ++m) {
+#pragma unroll
+      for (int j = 0; j < kSub; ++j) step(m * kSub + j, h0, at[0]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        sh.mid[m][n][tid] = make_float4(h0[n][0].x, h0[n][0].y, h0[n][1].x, h0[n][1].y);
+    }
+    float cs[MC] = {}, cb[MC] = {};  // the chunk's sums for dskip and dbias
+#pragma unroll 1
+    for (int m = subs - 1; m >= 0; --m) {
+      if (m > 0) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float4 f = sh.mid[m - 1][n][tid];
+          hs[0][n][0] = make_float2(f.x, f.y);
+          hs[0][n][1] = make_float2(f.z, f.w);
+        }
       } else {
+        load_lane(a.checkpoints + ((row * d.chunks + t0 / kChunk) * d.D + c0) * d.N, hs[0]);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[j + 1][i] = h[j][i];
+      for (int j = 0; j < kSub; ++j) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) hs[j + 1][n][0] = hs[j][n][0], hs[j + 1][n][1] = hs[j][n][1];
+        step(m * kSub + j, hs[j + 1], at[j]);
+      }
+#pragma unroll
+      for (int j = kSub - 1; j >= 0; --j) {
+        const int s = m * kSub + j;
+        const float4 d4 = *reinterpret_cast<const float4*>(&sh.d[s][ch]);
+        const float4 u4 = *reinterpret_cast<const float4*>(&sh.u[s][ch]);
+        const float4 y4 = *reinterpret_cast<const float4*>(&sh.dy[s][ch]);
+        const float4 b4 = *reinterpret_cast<const float4*>(&sh.B[s][n0]);
+        const float4 c4 = *reinterpret_cast<const float4*>(&sh.C[s][n0]);
+        const float2 d2[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
+        const float2 x2[2] = {__fmul2_rn(d2[0], make_float2(u4.x, u4.y)), __fmul2_rn(d2[1], make_float2(u4.z, u4.w))};
+        const float2 y2[2] = {make_float2(y4.x, y4.y), make_float2(y4.z, y4.w)};
+        const float b[4] = {b4.x, b4.y, b4.z, b4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
+        float2 gA[2] = {two(0.f), two(0.f)}, gB[2] = {two(0.f), two(0.f)}, y[2] = {two(0.f), two(0.f)};
+        float v[8];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) gr[n][p] = __ffma2_rn(two(c[n]), y2[p], gr[n][p]);
+          const float2 tb2 = __ffma2_rn(x2[1], gr[n][1], __fmul2_rn(x2[0], gr[n][0]));
+          const float2 tc2 = __ffma2_rn(y2[1], hs[j + 1][n][1], __fmul2_rn(y2[0], hs[j + 1][n][0]));
+          v[n] = tb2.x + tb2.y;
+          v[4 + n] = tc2.x + tc2.y;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            y[p] = __ffma2_rn(two(c[n]), hs[j + 1][n][p], y[p]);
+            gB[p] = __ffma2_rn(two(b[n]), gr[n][p], gB[p]);
+            gr[n][p] = __fmul2_rn(gr[n][p], at[j][n][p]);
+            const float2 w = __fmul2_rn(gr[n][p], hs[j][n][p]);
+            gA[p] = __ffma2_rn(w, A2[n][p], gA[p]);
+            dA[n][p] = __ffma2_rn(w, d2[p], dA[n][p]);
+          }
+        }
+        constexpr int CG = 32 / LN;
+        sum_over<8, CG, LN>(v, lane);
+        {
+          constexpr int NB = CG < 8 ? 8 / CG : 1;  // values the lane now has
+          const int cg = lane / LN;
+          int idx = 0;
+#pragma unroll
+          for (int bit = 0; (1 << bit) < (CG < 8 ? CG : 8); ++bit) idx += (cg >> bit & 1) * (4 >> bit);
+          if (CG <= 8 || cg < 8)
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              const int id = idx + i;  // B or C, state
+              sh.bc[warp][s][id / 4 * S::NP + n0 + id % 4] = v[i];
+            }
+        }
+        float r[12];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          r[3 * i] = i % 2 ? gA[i / 2].y : gA[i / 2].x;
+          r[3 * i + 1] = i % 2 ? gB[i / 2].y : gB[i / 2].x;
+          r[3 * i + 2] = i % 2 ? y[i / 2].y : y[i / 2].x;
+        }
+        sum_over12<LN>(r, lane);
+        if (writes && t0 + s < end)
+#pragma unroll
+          for (int i = 0; i < MC; ++i) {
+            const int k = mine + i;
+            const float u = sh.u[s][k], dyk = sh.dy[s][k];
+            const float dr = fmaf(r[3 * i], kLn2, r[3 * i + 1] * u) * sh.slope[s][k];
+            cs[i] = fmaf(dyk, u, cs[i]);
+            cb[i] += dr;
+            if (k < left) {
+              const int64_t t = t0 + s;
+              pdu[t * g.du.step + i] = from_f<T>(fmaf(r[3 * i + 1], sh.d[s][k], skip[i] * dyk));
+              pdd[t * g.ddelta.step + i] = from_f<T>(dr);
+              if (gate) pdz[t * g.dz.step + i] = from_f<T>(sh.zf[s][k] * fmaf(skip[i], u, r[3 * i + 2]));
+            }
+          }
       }
     }
-    for (int j = kChunk - 1; j >= 0; --j) {
-      const int64_t t = t0 + j;
-      if (t >= d.T) continue;
-      float bc[2][4] = {};
-      if (t >= len) {
-        if (p.on && lane == 0) {
-          du[t * g.du.step] = from_f<T>(0.f);
-          dd[t * g.ddelta.step] = from_f<T>(0.f);
-          if (z) dz[t * g.dz.step] = from_f<T>(0.f);
-        }
-      } else {
-        const float ut = to_f(u[t * a.u.step]);
-        const float raw = to_f(dl[t * a.delta.step]) + bias;
-        const float dt = a.flags & ZO_SCAN_SOFTPLUS ? softplus_f(raw) : raw;
-        float Bt[4], Ct[4], y = 0.f;
-        load_states(B + t * a.B.step, p.n0, d.N, Bt);
-        load_states(C + t * a.C.step, p.n0, d.N, Ct);
-        float dy = to_f(dout[t * g.dout.step]);
-        if (z) {
-          const float zt = to_f(z[t * a.z.step]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y = fmaf(Ct[i], h[j + 1][i], y);
-          y = fmaf(skip, ut, sum_lanes<LN>(y));
-          if (p.on && lane == 0) dz[t * g.dz.step] = from_f<T>(dy * y * dsilu_f(zt));
-          dy *= silu_f(zt);
-        }
-        float gB = 0.f, gA = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float at = expf(dt * A[i]);
-          gr[i] = fmaf(Ct[i], dy, gr[i]);
-          bc[0][i] = p.on ? gr[i] * dt * ut : 0.f;
-          bc[1][i] = p.on ? dy * h[j + 1][i] : 0.f;
-          gB = fmaf(gr[i], Bt[i], gB);
-          const float w = gr[i] * at * h[j][i];
-          gA = fmaf(w, A[i], gA);
-          dA[i] = fmaf(w, dt, dA[i]);
-          gr[i] *= at;
-        }
-        gB = sum_lanes<LN>(gB);
-        gA = sum_lanes<LN>(gA);
-        const float sp = a.flags & ZO_SCAN_SOFTPLUS ? sigmoid_f(raw) : 1.f;
-        const float dr = fmaf(gB, ut, gA) * sp;
-        ds = fmaf(dy, ut, ds);
-        db += dr;
-        if (p.on && lane == 0) {
-          du[t * g.du.step] = from_f<T>(fmaf(gB, dt, skip * dy));
-          dd[t * g.ddelta.step] = from_f<T>(dr);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int m = LN; m < 32; m *= 2) bc[q][i] += __shfl_xor_sync(0xffffffffu, bc[q][i], m);
-          if ((int)threadIdx.x % 32 < LN)
-            sh[((warp * kChunk + j) * 2 + q) * 4 * LN + p.n0 + i] = bc[q][i];
-        }
+    for (int i = 0; i < MC; ++i) {
+      ds[i] += cs[i];
+      db[i] += cb[i];
     }
     __syncthreads();
-    // [tile][row][t][g][dB, dC][N]
-    for (int i = threadIdx.x; i < kChunk * 2 * d.N; i += kThreads) {
-      const int n = i % d.N, q = i / d.N % 2, j = i / d.N / 2;
-      if (t0 + j < d.T) {
+    // [tile][row][t][group][dB, dC][N]
+    for (int i = tid; i < kChunk * 2 * d.N; i += S::kThreads) {
+      const int n = i % d.N, k = i / d.N % 2, s = i / d.N / 2;
+      if (t0 + s < end) {
         float v = 0.f;
-        for (int w = 0; w < kThreads / 32; ++w) v += sh[((w * kChunk + j) * 2 + q) * 4 * LN + n];
-        part_bc[((((int64_t)p.tile * a.rows + p.row) * d.T + t0 + j) * d.G + p.g) * 2 * d.N +
-                q * d.N + n] = v;
+#pragma unroll
+        for (int w = 0; w < S::kWarps; ++w) v += sh.bc[w][s][k * S::NP + n];
+        sums.bc[((((int64_t)tile * a.rows + row) * d.T + t0 + s) * d.G + grp) * 2 * d.N + k * d.N + n] = v;
       }
     }
-    __syncthreads();
+    if (++chunks % kFlush == 0) put_away();
   }
-  if (!p.on) return;
-  float* pa = part_a + p.row * d.D * d.N + cn;
-  float* di = g.dstate_in.ptr ? g.dstate_in.ptr + p.row * g.dstate_in.stride + cn : nullptr;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (p.n0 + i < d.N) {
-      pa[p.n0 + i] = dA[i];
-      if (di) di[p.n0 + i] = gr[i];
-    }
-  if (lane == 0) {
-    part_skip[p.row * d.D + p.c] = ds;
-    part_bias[p.row * d.D + p.c] = db;
-  }
+  while (flush < sums.flushes) put_away();
+  if (part == 0 && g.dstate_in.ptr)
+    store_lane(g.dstate_in.ptr + row * g.dstate_in.stride + c0 * d.N, gr);
 }
 
 template <class T>
@@ -663,8 +1018,9 @@ __global__ void __launch_bounds__(256)
   const int64_t per_step = (int64_t)d.G * 2 * d.N, n = a.rows * d.T * per_step;
   if (i >= n) return;
   float v = 0.f;
-  for (int t = 0; t < d.tiles; ++t) v += part[t * n + i];
   const int64_t row = i / per_step / d.T, t = i / per_step % d.T;
+  if (t < row_length(a.lengths, row, d.T, nullptr, false))
+    for (int k = 0; k < d.tiles; ++k) v += part[k * n + i];
   const int j = (int)(i % per_step), grp = j / (2 * d.N), q = j / d.N % 2, k = j % d.N;
   const zo_tensor& o = q ? g.dC : g.dB;
   static_cast<T*>(o.ptr)[row * o.row + t * o.step + (int64_t)grp * d.N + k] = from_f<T>(v);
@@ -787,32 +1143,79 @@ cudaError_t run_scan_step(const zo_scan_args& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <class T, int LN>
+// The backward pass's division of time: as scan_plan, for its own blocks.
+struct BackPlan {
+  int tiles, parts, steps, flushes;
+  int64_t bc, A, skip, state, sum;  // floats of workspace
+};
+template <int LN>
+BackPlan back_plan(const zo_scan_args& a) {
+  using S = BackTile<LN>;
+  BackPlan p;
+  p.tiles = (int)ceil_div(a.channels / a.groups, S::kChannels);
+  const int64_t blocks = (int64_t)p.tiles * a.groups * a.rows;
+  const int64_t room = 12 / S::kWarps * kBlockSMs;  // blocks that the SMs hold
+  int64_t n = blocks * 2 < room ? room / blocks : 1;
+  int64_t steps = ceil_div(ceil_div(a.seq, n), kChunk) * kChunk;
+  if (n > 1 && steps < 64) steps = 64;
+  p.parts = (int)ceil_div(a.seq, steps);
+  p.steps = (int)steps;
+  p.flushes = (int)ceil_div(steps / kChunk, kFlush);
+  const int64_t DN = (int64_t)a.channels * a.states, each = (int64_t)a.rows * p.parts;
+  p.bc = (int64_t)p.tiles * a.rows * a.seq * a.groups * 2 * a.states;
+  p.A = each * p.flushes * DN;
+  p.skip = each * p.flushes * a.channels;
+  p.state = p.parts > 1 ? each * DN : 0;
+  p.sum = p.parts > 1 ? each * a.channels : 0;
+  return p;
+}
+
+template <class T, int LN, int S, int LC>
 cudaError_t run_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, float* ws,
                               cudaStream_t st) {
-  const ScanDims d = scan_dims<LN>(a);
-  const int64_t blocks = (int64_t)d.tiles * d.G * a.rows, DN = (int64_t)d.D * d.N;
+  using B = BackTile<LN>;
+  const BackPlan p = back_plan<LN>(a);
+  ScanDims d = scan_dims<LN>(a);
+  d.tiles = p.tiles;
+  const int64_t DN = (int64_t)d.D * d.N, blocks = (int64_t)p.tiles * d.G * a.rows * p.parts;
   const int64_t bc = (int64_t)a.rows * d.T * d.G * 2 * d.N;
   if (blocks > INT32_MAX || ceil_div(bc, 256) > INT32_MAX) return cudaErrorInvalidConfiguration;
-  float* pa = ws + d.tiles * bc;
-  float* ps = pa + a.rows * DN;
-  float* pb = ps + (int64_t)a.rows * d.D;
-  const int smem = kThreads / 32 * kChunk * 2 * 4 * LN * (int)sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(scan_backward_kernel<T, LN>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  scan_backward_kernel<T, LN><<<(unsigned)blocks, kThreads, smem, st>>>(a, g, d, ws, pa, ps, pb);
+  float* state = ws;  // first, for its alignment
+  float* pa = state + ceil_div(p.state, 4) * 4;
+  const BackSums sums{pa + p.A, pa, pa + p.A + p.bc, pa + p.A + p.bc + p.skip, p.flushes};
+  const Parts parts{p.parts, p.steps, state, pa + p.A + p.bc + 2 * p.skip};
+  cudaError_t e = cudaSuccess;
+  if (p.parts > 1) {
+    const ScanPlan f = scan_plan(a);  // its blocks' shape
+    ScanDims dc = d;
+    dc.tiles = f.tiles;
+    const int64_t carry = (int64_t)f.tiles * d.G * a.rows * (p.parts - 1);
+    if (carry > INT32_MAX) return cudaErrorInvalidConfiguration;
+    scan_carry_kernel<T, S, LC><<<(unsigned)carry, 32 * f.warps, 0, st>>>(a, g, dc, parts);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    carry_join_kernel<<<(unsigned)ceil_div(a.rows * DN, 256), 256, 0, st>>>(a, g, d, parts);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  bool vec = true;
+  for (const zo_tensor* t : {&a.u, &a.delta, &a.z, &g.dout})
+    vec = vec && vec_width(*t, sizeof(T), d.Dg, 4) == 4;
+  if ((e = cudaFuncSetAttribute(scan_backward_kernel<T, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(B))) != cudaSuccess)
+    return e;
+  scan_backward_kernel<T, LN><<<(unsigned)blocks, B::kThreads, sizeof(B), st>>>(a, g, d, parts, sums, vec);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  sum_bc_kernel<T><<<(unsigned)ceil_div(bc, 256), 256, 0, st>>>(a, g, d, ws);
+  sum_bc_kernel<T><<<(unsigned)ceil_div(bc, 256), 256, 0, st>>>(a, g, d, sums.bc);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t rows = d.rows_per_set;
-  e = launch_sum_parts(pa, a.sets, rows, DN, DN, g.dA.ptr, g.dA.stride, st);
+  const int64_t n = (int64_t)d.rows_per_set * p.parts * p.flushes;
+  e = launch_sum_parts(sums.A, a.sets, n, DN, DN, g.dA.ptr, g.dA.stride, st);
   if (e == cudaSuccess && g.dskip.ptr)
-    e = launch_sum_parts(ps, a.sets, rows, d.D, d.D, g.dskip.ptr, g.dskip.stride, st);
+    e = launch_sum_parts(sums.skip, a.sets, n, d.D, d.D, g.dskip.ptr, g.dskip.stride, st);
   if (e == cudaSuccess && g.ddelta_bias.ptr)
-    e = launch_sum_parts(pb, a.sets, rows, d.D, d.D, g.ddelta_bias.ptr, g.ddelta_bias.stride, st);
+    e = launch_sum_parts(sums.bias, a.sets, n, d.D, d.D, g.ddelta_bias.ptr, g.ddelta_bias.stride, st);
   return e;
 }
 
@@ -867,9 +1270,8 @@ int64_t scan_workspace(const zo_scan_args& a) {
 
 int64_t scan_backward_workspace(const zo_scan_args& a) {
   return by_lanes(a.states, [&](auto ln) {
-    const ScanDims d = scan_dims<decltype(ln)::value>(a);
-    return (int64_t)sizeof(float) * ((int64_t)d.tiles * a.rows * d.T * d.G * 2 * d.N +
-                                     (int64_t)a.rows * d.D * (d.N + 2));
+    const BackPlan p = back_plan<decltype(ln)::value>(a);
+    return (int64_t)sizeof(float) * (p.bc + p.A + 2 * p.skip + ceil_div(p.state, 4) * 4 + p.sum);
   });
 }
 
@@ -898,7 +1300,8 @@ cudaError_t launch_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, 
                                  cudaStream_t st) {
   return by_type(a.dtype, [&](auto t) {
     return by_lanes(a.states, [&](auto ln) {
-      return run_scan_backward<decltype(t), decltype(ln)::value>(a, g, ws, st);
+      constexpr int L = decltype(ln)::value;  // four states a lane; the carry's kernel has up to 16
+      return run_scan_backward<decltype(t), L, L == 1 ? 4 : L == 2 ? 8 : 16, L <= 4 ? 1 : L / 4>(a, g, ws, st);
     });
   });
 }
