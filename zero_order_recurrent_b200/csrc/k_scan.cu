@@ -52,6 +52,18 @@ __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 exp2_2(float2 x) { return make_float2(exp2_1(x.x), exp2_1(x.y)); }
 __device__ __forceinline__ float2 rcp_2(float2 x) { return make_float2(rcp_1(x.x), rcp_1(x.y)); }
 
+// 2^x, more exactly for |x| < 1/16: the special function unit's results there are too small by
+// 1e-7 of themselves on average (they are cut off, measured), which over the 1 / |x| steps
+// that such a decay lasts adds up to 1e-6 of a state.  A polynomial of degree 3, 1 at 0, with the least largest relative error up to 1/16
+// (2.7e-8; its coefficients are the solution of that linear programme).
+__device__ __forceinline__ float2 exp2_slow_2(float2 x) {
+  const float2 e = exp2_2(x);
+  float2 p = __ffma2_rn(x, two(0.0554962232708931f), two(0.2402576357126236f));
+  p = __ffma2_rn(x, p, two(0.6931472420692444f));
+  p = __ffma2_rn(x, p, two(1.f));
+  return make_float2(fabsf(x.x) < 0.0625f ? p.x : e.x, fabsf(x.y) < 0.0625f ? p.y : e.y);
+}
+
 // max(x, 0), NaN for NaN
 __device__ __forceinline__ float relu_nan(float x) {
   float y;
@@ -657,6 +669,7 @@ __global__ void __launch_bounds__(256) carry_join_kernel(zo_scan_args a, zo_scan
 }
 
 constexpr int kSub = 2;      // steps whose states and decays are in registers together
+constexpr int kBlock = 4;    // steps between states kept in shared memory
 constexpr int kFlush = 64;   // chunks after which the parameters' sums are put away
 
 template <int LN>
@@ -664,12 +677,12 @@ struct BackTile {
   static constexpr int kWarps = LN >= 4 ? 4 : LN;          // 128 channels a block, or less
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kWarpChannels = 128 / LN, kChannels = kWarps * kWarpChannels;
-  static constexpr int NP = 4 * LN, kMid = kChunk / kSub - 1;
+  static constexpr int NP = 4 * LN, kMid = kChunk / kBlock - 1;
   alignas(16) float d[kChunk][kChannels], u[kChunk][kChannels], dy[kChunk][kChannels];
   float slope[kChunk][kChannels], zf[kChunk][kChannels];   // softplus'(raw), dout silu'(z)
-  alignas(16) float B[kChunk][NP], C[kChunk][NP];
-  alignas(16) float4 mid[kMid][4][kThreads];               // the states before the later sub-blocks
-  float bc[kWarps][kChunk][2 * NP];                        // the warps' sums for dB and dC
+  alignas(16) float2 B[kChunk][NP], C[kChunk][NP];         // each twice, for pairs of channels
+  alignas(16) float4 mid[kMid][4][kThreads];               // the states before the later blocks
+  float bc[kWarps][kChunk / 2][2 * NP];                    // the warps' sums for dB and dC, half a chunk
 };
 
 // What the backward pass leaves to be summed up: dB and dC by channel tile, the parameters'
@@ -685,13 +698,11 @@ struct BackSums {
 // and warp where 16 states a lane would take 31 and 4 states of one channel a lane 37.
 //
 // Chunk by chunk backwards: the states are run forward from the chunk's checkpoint,
-// keeping those before each kSub steps in shared memory; then, backwards over those
-// sub-blocks, states and decays are run again into registers and the carry comes back
-// through them.  The exponentials are so done nearly twice, which is less than to
-// keep every state in memory.
-//
-// Bound: by count the special function unit (37 of its results for a value with 16
-// states), the multiply-add pipe and issue are about equal.
+// keeping those before each block of kBlock steps in shared memory; then, backwards over the
+// blocks and kSub steps at a time, states and decays are run again into registers and the carry
+// comes back through them.  The exponentials are so done 2.25 times, which costs less than to
+// keep every state in memory.  More steps in registers, or all states before kSub steps in
+// shared memory, leave two blocks an SM instead of three.
 template <class T, int LN>
 __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / LN / 2)
     scan_backward_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, Parts parts, BackSums sums, bool vec) {
@@ -863,36 +874,41 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
     for (int i = tid; i < kChunk * S::NP; i += S::kThreads) {
       const int s = i / S::NP, n = i % S::NP;
       const bool in = t0 + s < end && n < d.N;
-      sh.B[s][n] = in ? to_f(bB[(t0 + s) * a.B.step + n]) : 0.f;
-      sh.C[s][n] = in ? to_f(bC[(t0 + s) * a.C.step + n]) : 0.f;
+      sh.B[s][n] = two(in ? to_f(bB[(t0 + s) * a.B.step + n]) : 0.f);
+      sh.C[s][n] = two(in ? to_f(bC[(t0 + s) * a.C.step + n]) : 0.f);
     }
     float2 h0[4][2];
     load_lane(a.checkpoints + ((row * d.chunks + t0 / kChunk) * d.D + c0) * d.N, h0);
     __syncthreads();
 
-    auto step = [&](int s, float2 (&h)[4][2], float2 (&at)[4][2]) {
+    auto load4 = [&](const float2* p, float2 (&f)[4]) {
+      const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+      f[0] = make_float2(x.x, x.y), f[1] = make_float2(x.z, x.w);
+      f[2] = make_float2(y.x, y.y), f[3] = make_float2(y.z, y.w);
+    };
+    auto step = [&](auto slow, int s, float2 (&h)[4][2], float2 (&at)[4][2]) {
       const float4 dt = *reinterpret_cast<const float4*>(&sh.d[s][ch]);
       const float4 u = *reinterpret_cast<const float4*>(&sh.u[s][ch]);
-      const float4 b4 = *reinterpret_cast<const float4*>(&sh.B[s][n0]);
+      float2 b[4];
+      load4(&sh.B[s][n0], b);
       const float2 d2[2] = {make_float2(dt.x, dt.y), make_float2(dt.z, dt.w)};
       const float2 x2[2] = {__fmul2_rn(d2[0], make_float2(u.x, u.y)), __fmul2_rn(d2[1], make_float2(u.z, u.w))};
-      const float b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          at[n][p] = exp2_2(__fmul2_rn(d2[p], A2[n][p]));
-          h[n][p] = __ffma2_rn(at[n][p], h[n][p], __fmul2_rn(x2[p], two(b[n])));
+          const float2 x = __fmul2_rn(d2[p], A2[n][p]);
+          at[n][p] = decltype(slow)::value ? exp2_slow_2(x) : exp2_2(x);
+          h[n][p] = __ffma2_rn(at[n][p], h[n][p], __fmul2_rn(x2[p], b[n]));
         }
     };
     float2 hs[kSub + 1][4][2], at[kSub][4][2];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) hs[0][n][0] = h0[n][0], hs[0][n][1] = h0[n][1];
+    const int blocks = (end - t0 < kChunk ? end - t0 + kBlock - 1 : kChunk) / kBlock;
     const int subs = (end - t0 < kChunk ? end - t0 + kSub - 1 : kChunk) / kSub;
 #pragma unroll 1
-    for (int m = 0; m + 1 < subs; ++m) {
+    for (int m = 0; m + 1 < blocks; ++m) {
 #pragma unroll
-      for (int j = 0; j < kSub; ++j) step(m * kSub + j, h0, at[0]);
+      for (int j = 0; j < kBlock; ++j) step(std::false_type(), m * kBlock + j, h0, at[0]);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
         sh.mid[m][n][tid] = make_float4(h0[n][0].x, h0[n][0].y, h0[n][1].x, h0[n][1].y);
@@ -900,21 +916,26 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
     float cs[MC] = {}, cb[MC] = {};  // the chunk's sums for dskip and dbias
 #pragma unroll 1
     for (int m = subs - 1; m >= 0; --m) {
-      if (m > 0) {
+      constexpr int R = kBlock / kSub;
+      if (m >= R) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const float4 f = sh.mid[m - 1][n][tid];
+          const float4 f = sh.mid[m / R - 1][n][tid];
           hs[0][n][0] = make_float2(f.x, f.y);
           hs[0][n][1] = make_float2(f.z, f.w);
         }
       } else {
         load_lane(a.checkpoints + ((row * d.chunks + t0 / kChunk) * d.D + c0) * d.N, hs[0]);
       }
+#pragma unroll 1
+      for (int k = m / R * R; k < m; ++k)  // from the block's first step
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) step(std::false_type(), k * kSub + j, hs[0], at[0]);
 #pragma unroll
       for (int j = 0; j < kSub; ++j) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) hs[j + 1][n][0] = hs[j][n][0], hs[j + 1][n][1] = hs[j][n][1];
-        step(m * kSub + j, hs[j + 1], at[j]);
+        step(std::true_type(), m * kSub + j, hs[j + 1], at[j]);
       }
 #pragma unroll
       for (int j = kSub - 1; j >= 0; --j) {
@@ -922,26 +943,26 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
         const float4 d4 = *reinterpret_cast<const float4*>(&sh.d[s][ch]);
         const float4 u4 = *reinterpret_cast<const float4*>(&sh.u[s][ch]);
         const float4 y4 = *reinterpret_cast<const float4*>(&sh.dy[s][ch]);
-        const float4 b4 = *reinterpret_cast<const float4*>(&sh.B[s][n0]);
-        const float4 c4 = *reinterpret_cast<const float4*>(&sh.C[s][n0]);
+        float2 b[4], c[4];
+        load4(&sh.B[s][n0], b);
+        load4(&sh.C[s][n0], c);
         const float2 d2[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
         const float2 x2[2] = {__fmul2_rn(d2[0], make_float2(u4.x, u4.y)), __fmul2_rn(d2[1], make_float2(u4.z, u4.w))};
         const float2 y2[2] = {make_float2(y4.x, y4.y), make_float2(y4.z, y4.w)};
-        const float b[4] = {b4.x, b4.y, b4.z, b4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
         float2 gA[2] = {two(0.f), two(0.f)}, gB[2] = {two(0.f), two(0.f)}, y[2] = {two(0.f), two(0.f)};
         float v[8];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p) gr[n][p] = __ffma2_rn(two(c[n]), y2[p], gr[n][p]);
+          for (int p = 0; p < 2; ++p) gr[n][p] = __ffma2_rn(c[n], y2[p], gr[n][p]);
           const float2 tb2 = __ffma2_rn(x2[1], gr[n][1], __fmul2_rn(x2[0], gr[n][0]));
           const float2 tc2 = __ffma2_rn(y2[1], hs[j + 1][n][1], __fmul2_rn(y2[0], hs[j + 1][n][0]));
           v[n] = tb2.x + tb2.y;
           v[4 + n] = tc2.x + tc2.y;
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            y[p] = __ffma2_rn(two(c[n]), hs[j + 1][n][p], y[p]);
-            gB[p] = __ffma2_rn(two(b[n]), gr[n][p], gB[p]);
+            y[p] = __ffma2_rn(c[n], hs[j + 1][n][p], y[p]);
+            gB[p] = __ffma2_rn(b[n], gr[n][p], gB[p]);
             gr[n][p] = __fmul2_rn(gr[n][p], at[j][n][p]);
             const float2 w = __fmul2_rn(gr[n][p], hs[j][n][p]);
             gA[p] = __ffma2_rn(w, A2[n][p], gA[p]);
@@ -960,7 +981,7 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
               const int id = idx + i;  // B or C, state
-              sh.bc[warp][s][id / 4 * S::NP + n0 + id % 4] = v[i];
+              sh.bc[warp][s % (kChunk / 2)][id / 4 * S::NP + n0 + id % 4] = v[i];
             }
         }
         float r[12];
@@ -987,22 +1008,25 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
             }
           }
       }
+      if (m * kSub % (kChunk / 2) == 0) {  // [tile][row][t][group][dB, dC][N]
+        __syncthreads();
+        for (int i = tid; i < kChunk / 2 * 2 * d.N; i += S::kThreads) {
+          const int n = i % d.N, k = i / d.N % 2, s = i / d.N / 2;
+          const int64_t t = t0 + m * kSub + s;
+          if (t < end) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w) v += sh.bc[w][s][k * S::NP + n];
+            sums.bc[((((int64_t)tile * a.rows + row) * d.T + t) * d.G + grp) * 2 * d.N + k * d.N + n] = v;
+          }
+        }
+        __syncthreads();
+      }
     }
 #pragma unroll
     for (int i = 0; i < MC; ++i) {
       ds[i] += cs[i];
       db[i] += cb[i];
-    }
-    __syncthreads();
-    // [tile][row][t][group][dB, dC][N]
-    for (int i = tid; i < kChunk * 2 * d.N; i += S::kThreads) {
-      const int n = i % d.N, k = i / d.N % 2, s = i / d.N / 2;
-      if (t0 + s < end) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < S::kWarps; ++w) v += sh.bc[w][s][k * S::NP + n];
-        sums.bc[((((int64_t)tile * a.rows + row) * d.T + t0 + s) * d.G + grp) * 2 * d.N + k * d.N + n] = v;
-      }
     }
     if (++chunks % kFlush == 0) put_away();
   }
