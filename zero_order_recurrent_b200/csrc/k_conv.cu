@@ -223,30 +223,44 @@ __global__ void __launch_bounds__(kThreads)
   store_vec<float, V>(out + (int64_t)K * d.D, db);
 }
 
-// 32 neighbouring values by 8 threads each, which take every eighth part.
-__global__ void __launch_bounds__(256)
-    sum_parts_kernel(const float* part, int64_t parts, int64_t part_stride, int64_t n, float* out,
-                     int64_t out_stride, int64_t set_stride) {
-  __shared__ float sh[8][33];
+struct SumOuts {
+  float* out[3];
+  int64_t stride[3], n[3];
+};
+
+// 32 neighbouring values a block, by G warps that take every G-th part, eight loads at a time.
+template <int G>
+__global__ void __launch_bounds__(32 * G)
+    sum_parts_kernel(const float* part, int64_t parts, int64_t n, SumOuts o) {
+  __shared__ float sh[G][33];
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-  const int64_t i = (int64_t)blockIdx.x * 32 + lane;
-  const float* p = part + (int64_t)blockIdx.y * set_stride;
-  float s0 = 0.f, s1 = 0.f;
+  const int64_t i = (int64_t)blockIdx.x * 32 + lane, set = blockIdx.y;
+  const float* p = part + set * parts * n + i;
+  float s = 0.f;
   if (i < n) {
     int64_t k = grp;
-    for (; k + 8 < parts; k += 16) {
-      s0 += p[k * part_stride + i];
-      s1 += p[(k + 8) * part_stride + i];
+    for (; k + 7 * G < parts; k += 8 * G) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = p[(k + j * G) * n];
+#pragma unroll
+      for (int j = 4; j > 0; j /= 2)
+#pragma unroll
+        for (int m = 0; m < j; ++m) v[m] += v[m + j];
+      s += v[0];
     }
-    if (k < parts) s0 += p[k * part_stride + i];
+    for (; k < parts; k += G) s += p[k * n];
   }
-  sh[grp][lane] = s0 + s1;
+  sh[grp][lane] = s;
   __syncthreads();
   if (grp == 0 && i < n) {
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v += sh[k][lane];
-    out[(int64_t)blockIdx.y * out_stride + i] = v;
+    for (int k = 0; k < G; ++k) v += sh[k][lane];
+    int64_t j = i;
+    int w = 0;
+    while (w < 2 && j >= o.n[w]) j -= o.n[w++];
+    if (o.out[w]) o.out[w][set * o.stride[w] + j] = v;
   }
 }
 
@@ -295,11 +309,8 @@ cudaError_t run_conv_backward(const zo_conv_args& a, const zo_conv_grads& g, flo
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t parts = (int64_t)d.rows_per_set * d.runs, n = (int64_t)(K + 1) * d.D;
-  e = launch_sum_parts(ws, a.sets, parts, n, (int64_t)K * d.D, g.dweight.ptr, g.dweight.stride, st);
-  if (e != cudaSuccess || !g.dbias.ptr) return e;
-  return launch_sum_parts(ws + (int64_t)K * d.D, a.sets, parts, n, d.D, g.dbias.ptr,
-                          g.dbias.stride, st);
+  const SumOut outs[2] = {{g.dweight, (int64_t)K * d.D}, {g.dbias, d.D}};
+  return launch_sum_parts(ws, a.sets, (int64_t)d.rows_per_set * d.runs, (int64_t)(K + 1) * d.D, outs, 2, st);
 }
 
 template <template <class, int, int> class F, class T, int V, class... A>
@@ -350,16 +361,27 @@ cudaError_t conv_backward_typed(const zo_conv_args& a, const zo_conv_grads& g, f
 
 }  // namespace
 
-cudaError_t launch_sum_parts(const float* part, int sets, int64_t parts, int64_t part_stride,
-                             int64_t n, float* out, int64_t out_stride, cudaStream_t st) {
+cudaError_t launch_sum_parts(const float* part, int sets, int64_t parts, int64_t n,
+                             const SumOut* outs, int count, cudaStream_t st) {
+  SumOuts o{};
+  for (int i = 0; i < count; ++i) {
+    o.out[i] = outs[i].out.ptr;
+    o.stride[i] = outs[i].out.stride;
+    o.n[i] = outs[i].n;
+  }
   const int64_t bx = ceil_div(n, 32);
   if (bx > INT32_MAX) return cudaErrorInvalidConfiguration;
   for (int s0 = 0; s0 < sets; s0 += 65535) {  // grid.y holds 16 bits
     const int ns = sets - s0 < 65535 ? sets - s0 : 65535;
-    sum_parts_kernel<<<dim3((unsigned)bx, (unsigned)ns), 256, 0, st>>>(
-        part + (int64_t)s0 * parts * part_stride, parts, part_stride, n,
-        out + (int64_t)s0 * out_stride, out_stride, parts * part_stride);
+    const dim3 grid((unsigned)bx, (unsigned)ns);
+    const float* p = part + (int64_t)s0 * parts * n;
+    if (parts > 64)
+      sum_parts_kernel<32><<<grid, 1024, 0, st>>>(p, parts, n, o);
+    else
+      sum_parts_kernel<8><<<grid, 256, 0, st>>>(p, parts, n, o);
     count_launch();
+    for (int i = 0; i < count; ++i)
+      if (o.out[i]) o.out[i] += 65535 * o.stride[i];
   }
   return cudaGetLastError();
 }

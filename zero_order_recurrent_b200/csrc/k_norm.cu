@@ -280,11 +280,9 @@ cudaError_t run_norm_backward(const zo_norm_args& a, const zo_norm_grads& g, flo
   count_launch();
   cudaError_t e = cudaGetLastError();
   const int64_t D = a.channels;
-  const zo_f32* sums[3] = {&g.dw_pre, &g.dw_post, &g.dscale};
-  for (int k = 0; k < 3 && e == cudaSuccess; ++k)
-    if (sums[k]->ptr)
-      e = launch_sum_parts(ws + k * D, a.sets, groups, 3 * D, D, sums[k]->ptr, sums[k]->stride, st);
-  return e;
+  if (e != cudaSuccess) return e;
+  const SumOut outs[3] = {{g.dw_pre, D}, {g.dw_post, D}, {g.dscale, D}};
+  return launch_sum_parts(ws, a.sets, groups, 3 * D, outs, 3, st);
 }
 
 // Whether all rows start on 16 bytes.

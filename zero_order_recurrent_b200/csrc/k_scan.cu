@@ -465,6 +465,8 @@ __global__ void __launch_bounds__(128, 4)
   }
 }
 
+constexpr int kJoin = 8;  // parts whose results are loaded together
+
 // state[row][k] becomes the state that part k starts from.
 __global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims d, Parts parts) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, DN = (int64_t)d.D * d.N;
@@ -472,15 +474,22 @@ __global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims
   const int64_t row = i / DN, cn = i % DN, c = cn / d.N, set = row / d.rows_per_set;
   const float A2 = a.A.ptr[set * a.A.stride + cn] * kLog2e;
   float h = a.state_in.ptr ? a.state_in.ptr[row * a.state_in.stride + cn] : 0.f;
-  for (int k = 0; k < parts.n; ++k) {
-    const int64_t at = row * parts.n + k;
-    float l = 0.f, s = 0.f;
-    if (k + 1 < parts.n) {
-      l = parts.state[at * DN + cn];
-      s = parts.sum[at * d.D + c];
-    }
-    parts.state[at * DN + cn] = h;
-    h = fmaf(exp2_1(s * A2), h, l);
+  float* state = parts.state + row * parts.n * DN + cn;
+  const float* sum = parts.sum + row * parts.n * d.D + c;
+  for (int k0 = 0; k0 < parts.n; k0 += kJoin) {
+    float l[kJoin], s[kJoin];
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j)
+      if (k0 + j + 1 < parts.n) {
+        l[j] = state[(k0 + j) * DN];
+        s[j] = sum[(int64_t)(k0 + j) * d.D];
+      }
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j)
+      if (k0 + j < parts.n) {
+        state[(k0 + j) * DN] = h;
+        h = fmaf(exp2_1(s[j] * A2), h, l[j]);
+      }
   }
 }
 
@@ -573,9 +582,10 @@ __device__ __forceinline__ void sum_over12(float* v, int lane) {
 // carry <- a_t (carry + C_t dy_t), t backwards; parts 1 .. n-1, into parts.state and sum.
 template <class T, int S, int LN>
 __global__ void __launch_bounds__(128, 4)
-    scan_carry_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, Parts parts) {
+    scan_carry_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, Parts parts, int copy) {
   constexpr int NP = S * LN, W = 32 / LN, H = S / 2;
   __shared__ __align__(16) float C[kTile][NP];
+  __shared__ __align__(16) T raw[kTile][NP];
   const unsigned tiles = d.tiles * d.G;
   const unsigned tile_g = blockIdx.x % tiles, rest = blockIdx.x / tiles;
   const int part = 1 + rest % (parts.n - 1), row = rest / (parts.n - 1);
@@ -595,42 +605,66 @@ __global__ void __launch_bounds__(128, 4)
   const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[set * a.delta_bias.stride + c] : 0.f;
   const bool softplus = a.flags & ZO_SCAN_SOFTPLUS, gate = a.z.ptr;
   const int len = (int)row_length(a.lengths, row, d.T, nullptr, false), end = len < te ? len : te;
-  const T* pd = static_cast<const T*>(a.delta.ptr) + row * a.delta.row + c;
-  const T* pz = static_cast<const T*>(a.z.ptr) + (gate ? row * a.z.row + c : 0);
-  const T* po = static_cast<const T*>(g.dout.ptr) + row * g.dout.row + c;
+  const int t1 = tb + (end > tb ? (end - 1 - tb) / kTile * kTile : -kTile);  // the last tile
+  const T* pd = static_cast<const T*>(a.delta.ptr) + row * a.delta.row + (int64_t)(t1 + kTile) * a.delta.step + c;
+  const T* po = static_cast<const T*>(g.dout.ptr) + row * g.dout.row + (int64_t)(t1 + kTile) * g.dout.step + c;
+  const T* pz = gate ? static_cast<const T*>(a.z.ptr) + row * a.z.row + (int64_t)(t1 + kTile) * a.z.step + c : nullptr;
   const T* pc = static_cast<const T*>(a.C.ptr) + row * a.C.row + (int64_t)grp * d.N;
+  T rd[kAhead], ro[kAhead], rz[kAhead];
+  auto load = [&](int t) {  // steps t .. t + kAhead - 1, those before the last loaded ones
+    pd -= kAhead * a.delta.step;
+    po -= kAhead * g.dout.step;
+    if (gate) pz -= kAhead * a.z.step;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (t >= tb && t + j < end) {
+        rd[j] = pd[j * a.delta.step];
+        ro[j] = po[j * g.dout.step];
+        if (gate) rz[j] = pz[j * a.z.step];
+      }
+  };
+  auto fetch = [&](int t) {
+    fetch_rows<T, NP>(&raw[0][0], pc + t * a.C.step, a.C.step, end - t < kTile ? end - t : kTile, d.N, copy);
+  };
   float sum = 0.f;
-  for (int t = tb + (end > tb ? (end - 1 - tb) / kTile * kTile : -kTile); t >= tb; t -= kTile) {
+  if (t1 >= tb) {
+    load(t1 + kTile - kAhead);
+    fetch(t1);
+  }
+  for (int t = t1; t >= tb; t -= kTile) {
+    copies_done();
     __syncthreads();
-    for (int i = threadIdx.x; i < kTile * NP; i += blockDim.x) {
-      const int s = i / NP, n = i % NP;
-      C[s][n] = t + s < end && n < d.N ? to_f(pc[(t + s) * a.C.step + n]) : 0.f;
+    for (int i = threadIdx.x; i < kTile * NP / 4; i += blockDim.x) {
+      const int n = i % (NP / 4) * 4;
+      float f[4];
+      load_vec<T, 4>(&raw[0][0] + i * 4, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j >= d.N || t + i / (NP / 4) >= end) f[j] = 0.f;
+      store_vec<float, 4>(&C[0][0] + i * 4, f);
     }
     __syncthreads();
+    if (t > tb) fetch(t - kTile);
 #pragma unroll 1
-    for (int s = kTile - 4; s >= 0; s -= 4) {
-      float2 dt[2], dy[2];
+    for (int s = kTile - kAhead; s >= 0; s -= kAhead) {
+      const int n = end - t - s;  // steps that exist
+      float2 dt[kAhead / 2], dy[kAhead / 2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float rd[2], ro[2], rz[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int64_t u = t + s + 2 * j + e;
-          const bool in = u < end;
-          rd[e] = in ? to_f(pd[u * a.delta.step]) : 0.f;
-          ro[e] = in ? to_f(po[u * g.dout.step]) : 0.f;
-          rz[e] = in && gate ? to_f(pz[u * a.z.step]) : 0.f;
-        }
-        dt[j] = __fadd2_rn(make_float2(rd[0], rd[1]), two(bias));
-        if (softplus) dt[j] = softplus_2(dt[j]);
-        if (t + s + 2 * j >= end) dt[j].x = 0.f;
-        if (t + s + 2 * j + 1 >= end) dt[j].y = 0.f;
-        dy[j] = make_float2(ro[0], ro[1]);
-        if (gate) dy[j] = __fmul2_rn(dy[j], silu_2(make_float2(rz[0], rz[1])));
-        sum += dt[j].x + dt[j].y;
+      for (int j = 0; j < kAhead; j += 2) {
+        dt[j / 2] = __fadd2_rn(make_float2(to_f(rd[j]), to_f(rd[j + 1])), two(bias));
+        dy[j / 2] = make_float2(j < n ? to_f(ro[j]) : 0.f, j + 1 < n ? to_f(ro[j + 1]) : 0.f);
+        if (gate)
+          dy[j / 2] = __fmul2_rn(dy[j / 2], silu_2(make_float2(j < n ? to_f(rz[j]) : 0.f, j + 1 < n ? to_f(rz[j + 1]) : 0.f)));
       }
+      load(t + s - kAhead);
 #pragma unroll
-      for (int j = 3; j >= 0; --j) {
+      for (int j = kAhead - 1; j >= 0; --j) {
+        if (j % 2) {
+          if (softplus) dt[j / 2] = softplus_2(dt[j / 2]);
+          if (j - 1 >= n) dt[j / 2].x = 0.f;
+          if (j >= n) dt[j / 2].y = 0.f;
+          sum += dt[j / 2].x + dt[j / 2].y;
+        }
         const float2 d1 = two(j % 2 ? dt[j / 2].y : dt[j / 2].x), y1 = two(j % 2 ? dy[j / 2].y : dy[j / 2].x);
         const float4* cs = reinterpret_cast<const float4*>(&C[s + j][n0]);
 #pragma unroll
@@ -656,15 +690,22 @@ __global__ void __launch_bounds__(256) carry_join_kernel(zo_scan_args a, zo_scan
   const int64_t row = i / DN, cn = i % DN, c = cn / d.N, set = row / d.rows_per_set;
   const float A2 = a.A.ptr[set * a.A.stride + cn] * kLog2e;
   float v = g.dstate_out.ptr ? g.dstate_out.ptr[row * g.dstate_out.stride + cn] : 0.f;
-  for (int k = parts.n - 1; k >= 0; --k) {
-    const int64_t at = row * parts.n + k;
-    float l = 0.f, s = 0.f;
-    if (k > 0) {
-      l = parts.state[at * DN + cn];
-      s = parts.sum[at * d.D + c];
-    }
-    parts.state[at * DN + cn] = v;
-    v = fmaf(exp2_1(s * A2), v, l);
+  float* state = parts.state + row * parts.n * DN + cn;
+  const float* sum = parts.sum + row * parts.n * d.D + c;
+  for (int k0 = parts.n - 1; k0 >= 0; k0 -= kJoin) {
+    float l[kJoin], s[kJoin];
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j)
+      if (k0 - j > 0) {
+        l[j] = state[(k0 - j) * DN];
+        s[j] = sum[(int64_t)(k0 - j) * d.D];
+      }
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j)
+      if (k0 - j >= 0) {
+        state[(k0 - j) * DN] = v;
+        v = fmaf(exp2_1(s[j] * A2), v, l[j]);
+      }
   }
 }
 
@@ -688,8 +729,8 @@ struct BackTile {
 // What the backward pass leaves to be summed up: dB and dC by channel tile, the parameters'
 // gradients by row, part and flush.
 struct BackSums {
-  float *bc, *A, *skip, *bias;
-  int flushes;  // of a row's part
+  float *bc, *param;  // param: [row, part, flush][D N of A, D of skip, D of the bias]
+  int flushes;        // of a row's part
 };
 
 // A lane holds 4 neighbouring channels x 4 states, in pairs of channels: so the sums
@@ -793,14 +834,15 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
   int flush = 0;
   auto put_away = [&] {  // the parameters' sums so far
     const int64_t at = ((int64_t)row * parts.n + part) * sums.flushes + flush++;
-    store_lane(sums.A + (at * d.D + c0) * d.N, dA);
+    float* p = sums.param + at * ((int64_t)d.D * (d.N + 2));
+    store_lane(p + c0 * d.N, dA);
 #pragma unroll
     for (int n = 0; n < 4; ++n) dA[n][0] = dA[n][1] = two(0.f);
 #pragma unroll
     for (int i = 0; i < MC; ++i) {
       if (writes && mine + i < left) {
-        sums.skip[at * d.D + c0 + mine + i] = ds[i];
-        sums.bias[at * d.D + c0 + mine + i] = db[i];
+        p[(int64_t)d.D * d.N + c0 + mine + i] = ds[i];
+        p[(int64_t)d.D * (d.N + 1) + c0 + mine + i] = db[i];
       }
       ds[i] = db[i] = 0.f;
     }
@@ -813,13 +855,21 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
   const T* bB = static_cast<const T*>(a.B.ptr) + row * a.B.row + (int64_t)grp * d.N;
   const T* bC = static_cast<const T*>(a.C.ptr) + row * a.C.row + (int64_t)grp * d.N;
 
+  // A thread takes the same four channels of every step that it prepares.
+  constexpr int kQuads = S::kChannels / 4;
+  const int pc = tid % kQuads * 4;
+  float bias[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    bias[e] = a.delta_bias.ptr && pc + e < left ? a.delta_bias.ptr[set * a.delta_bias.stride + c0 + pc + e] : 0.f;
+
   int chunks = 0;
   for (int t0 = end > tb ? tb + (end - 1 - tb) / kChunk * kChunk : tb - 1; t0 >= tb; t0 -= kChunk) {
     __syncthreads();
     // The chunk's inputs and what is one channel's and step's, four channels at a time.
 #pragma unroll 2
-    for (int i = tid; i < kChunk * S::kChannels / 4; i += S::kThreads) {
-      const int s = i / (S::kChannels / 4), c = i % (S::kChannels / 4) * 4;
+    for (int s = tid / kQuads; s < kChunk; s += S::kThreads / kQuads) {
+      const int c = pc;
       const int64_t t = t0 + s;
       float fu[4] = {}, fd[4] = {}, fz[4] = {}, fo[4] = {};
       if (t < end) {
@@ -842,9 +892,7 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
       float o[5][4];
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        const float2 k = a.delta_bias.ptr ? make_float2(c + e < left ? a.delta_bias.ptr[set * a.delta_bias.stride + c0 + c + e] : 0.f,
-                                                        c + e + 1 < left ? a.delta_bias.ptr[set * a.delta_bias.stride + c0 + c + e + 1] : 0.f)
-                                          : two(0.f);
+        const float2 k = make_float2(bias[e], bias[e + 1]);
         const float2 raw = __fadd2_rn(make_float2(fd[e], fd[e + 1]), k);
         float2 dt = raw, slope = two(1.f), dy = make_float2(fo[e], fo[e + 1]), zf = two(0.f);
         if (softplus) {
@@ -914,6 +962,8 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
         sh.mid[m][n][tid] = make_float4(h0[n][0].x, h0[n][0].y, h0[n][1].x, h0[n][1].y);
     }
     float cs[MC] = {}, cb[MC] = {};  // the chunk's sums for dskip and dbias
+    const int64_t after = t0 + subs * kSub;
+    T *wu = pdu + after * g.du.step, *wd = pdd + after * g.ddelta.step, *wz = pdz + (gate ? after * g.dz.step : 0);
 #pragma unroll 1
     for (int m = subs - 1; m >= 0; --m) {
       constexpr int R = kBlock / kSub;
@@ -992,6 +1042,9 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
           r[3 * i + 2] = i % 2 ? y[i / 2].y : y[i / 2].x;
         }
         sum_over12<LN>(r, lane);
+        wu -= g.du.step;
+        wd -= g.ddelta.step;
+        if (gate) wz -= g.dz.step;
         if (writes && t0 + s < end)
 #pragma unroll
           for (int i = 0; i < MC; ++i) {
@@ -1001,10 +1054,9 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
             cs[i] = fmaf(dyk, u, cs[i]);
             cb[i] += dr;
             if (k < left) {
-              const int64_t t = t0 + s;
-              pdu[t * g.du.step + i] = from_f<T>(fmaf(r[3 * i + 1], sh.d[s][k], skip[i] * dyk));
-              pdd[t * g.ddelta.step + i] = from_f<T>(dr);
-              if (gate) pdz[t * g.dz.step + i] = from_f<T>(sh.zf[s][k] * fmaf(skip[i], u, r[3 * i + 2]));
+              wu[i] = from_f<T>(fmaf(r[3 * i + 1], sh.d[s][k], skip[i] * dyk));
+              wd[i] = from_f<T>(dr);
+              if (gate) wz[i] = from_f<T>(sh.zf[s][k] * fmaf(skip[i], u, r[3 * i + 2]));
             }
           }
       }
@@ -1170,7 +1222,7 @@ cudaError_t run_scan_step(const zo_scan_args& a, cudaStream_t st) {
 // The backward pass's division of time: as scan_plan, for its own blocks.
 struct BackPlan {
   int tiles, parts, steps, flushes;
-  int64_t bc, A, skip, state, sum;  // floats of workspace
+  int64_t bc, param, state, sum;  // floats of workspace
 };
 template <int LN>
 BackPlan back_plan(const zo_scan_args& a) {
@@ -1187,8 +1239,7 @@ BackPlan back_plan(const zo_scan_args& a) {
   p.flushes = (int)ceil_div(steps / kChunk, kFlush);
   const int64_t DN = (int64_t)a.channels * a.states, each = (int64_t)a.rows * p.parts;
   p.bc = (int64_t)p.tiles * a.rows * a.seq * a.groups * 2 * a.states;
-  p.A = each * p.flushes * DN;
-  p.skip = each * p.flushes * a.channels;
+  p.param = each * p.flushes * (DN + 2 * a.channels);
   p.state = p.parts > 1 ? each * DN : 0;
   p.sum = p.parts > 1 ? each * a.channels : 0;
   return p;
@@ -1205,9 +1256,9 @@ cudaError_t run_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, flo
   const int64_t bc = (int64_t)a.rows * d.T * d.G * 2 * d.N;
   if (blocks > INT32_MAX || ceil_div(bc, 256) > INT32_MAX) return cudaErrorInvalidConfiguration;
   float* state = ws;  // first, for its alignment
-  float* pa = state + ceil_div(p.state, 4) * 4;
-  const BackSums sums{pa + p.A, pa, pa + p.A + p.bc, pa + p.A + p.bc + p.skip, p.flushes};
-  const Parts parts{p.parts, p.steps, state, pa + p.A + p.bc + 2 * p.skip};
+  float* param = state + ceil_div(p.state, 4) * 4;
+  const BackSums sums{param + p.param, param, p.flushes};
+  const Parts parts{p.parts, p.steps, state, param + p.param + p.bc};
   cudaError_t e = cudaSuccess;
   if (p.parts > 1) {
     const ScanPlan f = scan_plan(a);  // its blocks' shape
@@ -1215,7 +1266,8 @@ cudaError_t run_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, flo
     dc.tiles = f.tiles;
     const int64_t carry = (int64_t)f.tiles * d.G * a.rows * (p.parts - 1);
     if (carry > INT32_MAX) return cudaErrorInvalidConfiguration;
-    scan_carry_kernel<T, S, LC><<<(unsigned)carry, 32 * f.warps, 0, st>>>(a, g, dc, parts);
+    scan_carry_kernel<T, S, LC><<<(unsigned)carry, 32 * f.warps, 0, st>>>(
+        a, g, dc, parts, copy_bytes({&a.C}, sizeof(T), d.N));
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     carry_join_kernel<<<(unsigned)ceil_div(a.rows * DN, 256), 256, 0, st>>>(a, g, d, parts);
@@ -1234,13 +1286,8 @@ cudaError_t run_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, flo
   sum_bc_kernel<T><<<(unsigned)ceil_div(bc, 256), 256, 0, st>>>(a, g, d, sums.bc);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t n = (int64_t)d.rows_per_set * p.parts * p.flushes;
-  e = launch_sum_parts(sums.A, a.sets, n, DN, DN, g.dA.ptr, g.dA.stride, st);
-  if (e == cudaSuccess && g.dskip.ptr)
-    e = launch_sum_parts(sums.skip, a.sets, n, d.D, d.D, g.dskip.ptr, g.dskip.stride, st);
-  if (e == cudaSuccess && g.ddelta_bias.ptr)
-    e = launch_sum_parts(sums.bias, a.sets, n, d.D, d.D, g.ddelta_bias.ptr, g.ddelta_bias.stride, st);
-  return e;
+  const SumOut outs[3] = {{g.dA, DN}, {g.dskip, d.D}, {g.ddelta_bias, d.D}};
+  return launch_sum_parts(sums.param, a.sets, (int64_t)d.rows_per_set * p.parts * p.flushes, DN + 2 * d.D, outs, 3, st);
 }
 
 // Lanes of a channel: four states each, a power of two.
@@ -1295,7 +1342,7 @@ int64_t scan_workspace(const zo_scan_args& a) {
 int64_t scan_backward_workspace(const zo_scan_args& a) {
   return by_lanes(a.states, [&](auto ln) {
     const BackPlan p = back_plan<decltype(ln)::value>(a);
-    return (int64_t)sizeof(float) * (p.bc + p.A + 2 * p.skip + ceil_div(p.state, 4) * 4 + p.sum);
+    return (int64_t)sizeof(float) * (p.bc + p.param + ceil_div(p.state, 4) * 4 + p.sum);
   });
 }
 

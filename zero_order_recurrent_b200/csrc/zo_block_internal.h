@@ -41,9 +41,14 @@ int64_t norm_backward_workspace(const zo_norm_args& a);
 cudaError_t launch_norm_backward(const zo_norm_args& a, const zo_norm_grads& g, float* ws,
                                  cudaStream_t st);
 
-// out[s][i] = sum over p < parts of part[(s parts + p) part_stride + i], i < n,
-// in a fixed order.
-cudaError_t launch_sum_parts(const float* part, int sets, int64_t parts, int64_t part_stride,
-                             int64_t n, float* out, int64_t out_stride, cudaStream_t st);
+// Partial sums are laid out [set][part][n values]; the values are those of up to three outputs
+// one after the other, each n long; outputs without a pointer are left out.  Every value
+// is the sum over the parts in a fixed order.
+struct SumOut {
+  zo_f32 out;
+  int64_t n;
+};
+cudaError_t launch_sum_parts(const float* part, int sets, int64_t parts, int64_t n,
+                             const SumOut* outs, int count, cudaStream_t st);
 
 }  // namespace zo
