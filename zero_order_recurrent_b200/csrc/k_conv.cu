@@ -3,10 +3,13 @@
 // results that the block's backward passes share.
 //
 // Bound: memory.  The forward reads x and writes out once (2 K + 6 flops for 2
-// values moved), the backward reads x and dout and writes dx.  A thread owns V
-// neighbouring channels (16 bytes of a row in the forward, 8 in the backward,
-// which keeps twice the windows) and walks a run of steps with the window in
-// registers, so x is read once per run plus K - 1 steps of overlap.
+// values moved), the backward reads x and dout and writes dx.  A thread owns four
+// neighbouring channels and walks a run of steps with the window in registers, in
+// pairs of channels for the packed fp32 instructions, so x is read once per run plus
+// K - 1 steps of overlap; the next U steps are on their way while U are computed.
+#include <initializer_list>
+#include <type_traits>
+
 #include "zo_block.cuh"
 #include "zo_block_internal.h"
 #include "zo_internal.h"
@@ -15,212 +18,274 @@ namespace zo {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int V = 4;  // channels a thread
 
 struct ConvDims {
-  int64_t T;
-  int D, rows_per_set, run, runs, ctiles;
+  int T, D, rows_per_set, run, runs, ctiles;
+  bool params;  // the parameters' rows start on 16 bytes
 };
 
-__device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t row, int64_t T,
-                                              int32_t* status, bool tell) {
+__device__ __forceinline__ int row_length(const int32_t* lengths, int64_t row, int T,
+                                          int32_t* status, bool tell) {
   if (!lengths) return T;
-  const int64_t n = lengths[row];
+  const int n = lengths[row];
   if (n >= 0 && n <= T) return n;
   if (status && tell) *status = ZO_ERR_BOUNDS;
   return n < 0 ? 0 : T;
 }
 
-// The window value at step p (may be before 0): x, or the carried state, or 0.
-template <class T, int V, int K>
-__device__ __forceinline__ void load_step(const T* x, int64_t x_step, const T* s, int64_t s_step,
-                                          int64_t p, int64_t len, float (&f)[V]) {
-  if (p >= 0 && p < len) {
-    load_vec<T, V>(x + p * x_step, f);
-  } else if (p < 0 && s) {
-    load_vec<T, V>(s + (p + K - 1) * s_step, f);
+// Four channels from p, of which `have` exist (VEC: always all, on a vector's boundary).
+template <class T, bool VEC>
+__device__ __forceinline__ Vec<T, V> load4(const T* p, int have) {
+  if constexpr (VEC) {
+    return *reinterpret_cast<const Vec<T, V>*>(p);
   } else {
+    Vec<T, V> x;
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = 0.f;
+    for (int i = 0; i < V; ++i) x.v[i] = i < have ? p[i] : from_f<T>(0.f);
+    return x;
   }
 }
 
-// U steps at a time: their loads are issued together.
-template <class T, int V, int K, int U>
-__global__ void __launch_bounds__(kThreads)
-    conv_kernel(zo_conv_args a, ConvDims d) {
-  const int ct = blockIdx.x % d.ctiles;
-  const int64_t rest = blockIdx.x / d.ctiles;
-  const int run = (int)(rest % d.runs);
-  const int64_t row = rest / d.runs;
-  const int64_t c = ((int64_t)ct * kThreads + threadIdx.x) * V;
-  if (c >= d.D) return;
-  const int64_t len = row_length(a.lengths, row, d.T, a.status, run == 0 && c == 0);
-  const T* x = static_cast<const T*>(a.x.ptr) + row * a.x.row + c;
-  const T* s = a.state_in.ptr ? static_cast<const T*>(a.state_in.ptr) + row * a.state_in.row + c
-                              : nullptr;
-  T* out = static_cast<T*>(a.out.ptr) + row * a.out.row + c;
-  const int64_t set = row / d.rows_per_set;
-  float w[K][V], b[V];
+template <class T, bool VEC>
+__device__ __forceinline__ void store4(T* p, int have, const float2 (&f)[2]) {
+  Vec<T, V> x;
+  x.v[0] = from_f<T>(f[0].x), x.v[1] = from_f<T>(f[0].y);
+  x.v[2] = from_f<T>(f[1].x), x.v[3] = from_f<T>(f[1].y);
+  if constexpr (VEC) {
+    *reinterpret_cast<Vec<T, V>*>(p) = x;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < have) p[i] = x.v[i];
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void pairs_of(const Vec<T, V>& x, float2 (&f)[2]) {
+  f[0] = make_float2(to_f(x.v[0]), to_f(x.v[1]));
+  f[1] = make_float2(to_f(x.v[2]), to_f(x.v[3]));
+}
+
+__device__ __forceinline__ void load_params(const float* p, int have, bool vec, float2 (&f)[2]) {
+  Vec<float, V> x;
+  if (vec) {
+    x = *reinterpret_cast<const Vec<float, V>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x.v[i] = i < have ? p[i] : 0.f;
+  }
+  pairs_of(x, f);
+}
+
+__device__ __forceinline__ void zero(float2 (&f)[2]) { f[0] = f[1] = two(0.f); }
+
+// Where a thread works.
+struct Place {
+  int run, c, have;
+  int64_t row, set;
+};
+__device__ __forceinline__ Place place(const ConvDims& d) {
+  Place p;
+  const unsigned rest = blockIdx.x / (unsigned)d.ctiles;
+  p.c = (int)((blockIdx.x % (unsigned)d.ctiles * kThreads + threadIdx.x) * V);
+  p.have = d.D - p.c;
+  p.run = rest % (unsigned)d.runs;
+  p.row = rest / (unsigned)d.runs;
+  p.set = (int)p.row / d.rows_per_set;
+  return p;
+}
+
+// One row's inputs: x, before it the carried window (or 0), after its length 0.
+template <class T, int K, bool VEC>
+struct Inputs {
+  const T *x, *s;
+  int64_t x_step, s_step;
+  int len, have;
+  __device__ __forceinline__ Inputs(const zo_conv_args& a, const Place& p, int n) {
+    x = static_cast<const T*>(a.x.ptr) + p.row * a.x.row + p.c;
+    s = K > 1 && a.state_in.ptr ? static_cast<const T*>(a.state_in.ptr) + p.row * a.state_in.row + p.c : nullptr;
+    x_step = a.x.step;
+    s_step = a.state_in.step;
+    len = n;
+    have = p.have;
+  }
+  __device__ __forceinline__ Vec<T, V> at(int t) const {
+    if (t >= 0 && t < len) return load4<T, VEC>(x + t * x_step, have);
+    if (t < 0 && s) return load4<T, VEC>(s + (t + K - 1) * s_step, have);
+    Vec<T, V> z;
+#pragma unroll
+    for (int i = 0; i < V; ++i) z.v[i] = from_f<T>(0.f);
+    return z;
+  }
+};
+
+template <class T, int K, int U, bool VEC>
+__global__ void __launch_bounds__(kThreads) conv_kernel(zo_conv_args a, ConvDims d) {
+  const Place p = place(d);
+  if (p.have <= 0) return;
+  const int len = row_length(a.lengths, p.row, d.T, a.status, p.run == 0 && p.c == 0);
+  const Inputs<T, K, VEC> in(a, p, len);
+  float2 w[K][2], b[2];
 #pragma unroll
   for (int k = 0; k < K; ++k)
+    load_params(a.weight.ptr + p.set * a.weight.stride + (int64_t)k * d.D + p.c, p.have, d.params, w[k]);
+  zero(b);
+  if (a.bias.ptr) load_params(a.bias.ptr + p.set * a.bias.stride + p.c, p.have, d.params, b);
+  const int t0 = p.run * d.run, t1 = t0 + d.run < d.T ? t0 + d.run : d.T;
+  Vec<T, V> next[U];
 #pragma unroll
-    for (int i = 0; i < V; ++i) w[k][i] = a.weight.ptr[set * a.weight.stride + (int64_t)k * d.D + c + i];
+  for (int j = 0; j < U; ++j) next[j] = in.at(t0 + j);
+  float2 win[K - 1 + U][2];
 #pragma unroll
-  for (int i = 0; i < V; ++i) b[i] = a.bias.ptr ? a.bias.ptr[set * a.bias.stride + c + i] : 0.f;
-  const int64_t t0 = (int64_t)run * d.run;
-  const int64_t t1 = t0 + d.run < d.T ? t0 + d.run : d.T;
-  float win[K - 1 + U][V];
-#pragma unroll
-  for (int j = 0; j < K - 1; ++j)
-    load_step<T, V, K>(x, a.x.step, s, a.state_in.step, t0 - (K - 1) + j, len, win[j]);
+  for (int j = 0; j < K - 1; ++j) pairs_of(in.at(t0 - (K - 1) + j), win[j]);
   const bool silu = a.flags & ZO_CONV_SILU;
-  for (int64_t t = t0; t < t1; t += U) {
+  T* out = static_cast<T*>(a.out.ptr) + p.row * a.out.row + (int64_t)t0 * a.out.step + p.c;
+  for (int t = t0; t < t1; t += U) {
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-      load_step<T, V, K>(x, a.x.step, s, a.state_in.step, t + j, len, win[K - 1 + j]);
+    for (int j = 0; j < U; ++j) pairs_of(next[j], win[K - 1 + j]);
+    if (t + U < t1)
+#pragma unroll
+      for (int j = 0; j < U; ++j) next[j] = in.at(t + U + j);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (t + j >= t1) break;
-      float y[V];
+      float2 y[2];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float p = b[i];
+      for (int i = 0; i < 2; ++i) {
+        y[i] = b[i];
 #pragma unroll
-        for (int k = 0; k < K; ++k) p = fmaf(w[k][i], win[j + k][i], p);
-        y[i] = t + j < len ? (silu ? silu_f(p) : p) : 0.f;
+        for (int k = 0; k < K; ++k) y[i] = __ffma2_rn(w[k][i], win[j + k][i], y[i]);
+        if (silu) y[i] = silu_2(y[i]);
+        if (t + j >= len) y[i] = two(0.f);
       }
-      store_vec<T, V>(out + (t + j) * a.out.step, y);
+      store4<T, VEC>(out, p.have, y);
+      out += a.out.step;
     }
 #pragma unroll
     for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) win[j][i] = win[U + j][i];
+      for (int i = 0; i < 2; ++i) win[j][i] = win[U + j][i];
   }
   // The window after the row's last step.  Only the first run reads state_in, so
   // the same thread may write it in place: all loads come before the stores.
-  if (K > 1 && run == 0 && a.state_out.ptr) {
-    T* so = static_cast<T*>(a.state_out.ptr) + row * a.state_out.row + c;
+  if (K > 1 && p.run == 0 && a.state_out.ptr) {
+    T* so = static_cast<T*>(a.state_out.ptr) + p.row * a.state_out.row + p.c;
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j)
-      load_step<T, V, K>(x, a.x.step, s, a.state_in.step, len - (K - 1) + j, len, win[j]);
+    for (int j = 0; j < K - 1; ++j) pairs_of(in.at(len - (K - 1) + j), win[j]);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) store_vec<T, V>(so + j * a.state_out.step, win[j]);
+    for (int j = 0; j < K - 1; ++j) store4<T, VEC>(so + j * a.state_out.step, p.have, win[j]);
   }
 }
 
 // d_t = dout_t silu'(pre_t);  dx_p = sum_k w[k] d_{p+K-1-k} (+ what state_out's
 // gradient sends to p);  dw[k] += d_t x_{t-K+1+k};  db += d_t.
-// The run of steps [t0, t1) owns d_t for the sums, and gives dx_p for
-// p = t - (K - 1), t in [t0, t1 + K - 1 if it is the last run): p < 0 is the
-// carried window's gradient.
-template <class T, int V, int K, int U>
+// The run of steps [t0, t1) owns d_t for the sums, and gives dx_p for p in [t0, t1);
+// the first run also for p < 0, which is the carried window's gradient.
+template <class T, int K, int U, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     conv_backward_kernel(zo_conv_args a, zo_conv_grads g, ConvDims d, float* part) {
-  const int ct = blockIdx.x % d.ctiles;
-  const int64_t rest = blockIdx.x / d.ctiles;
-  const int run = (int)(rest % d.runs);
-  const int64_t row = rest / d.runs;
-  const int64_t c = ((int64_t)ct * kThreads + threadIdx.x) * V;
-  if (c >= d.D) return;
-  const int64_t len = row_length(a.lengths, row, d.T, a.status, run == 0 && c == 0);
-  const T* x = static_cast<const T*>(a.x.ptr) + row * a.x.row + c;
-  const T* s = a.state_in.ptr ? static_cast<const T*>(a.state_in.ptr) + row * a.state_in.row + c
-                              : nullptr;
-  const T* dout = static_cast<const T*>(g.dout.ptr) + row * g.dout.row + c;
-  const T* dso = g.dstate_out.ptr
-                     ? static_cast<const T*>(g.dstate_out.ptr) + row * g.dstate_out.row + c
+  const Place p = place(d);
+  if (p.have <= 0) return;
+  const int len = row_length(a.lengths, p.row, d.T, a.status, p.run == 0 && p.c == 0);
+  const Inputs<T, K, VEC> in(a, p, len);
+  const T* dout = static_cast<const T*>(g.dout.ptr) + p.row * g.dout.row + p.c;
+  const T* dso = K > 1 && g.dstate_out.ptr
+                     ? static_cast<const T*>(g.dstate_out.ptr) + p.row * g.dstate_out.row + p.c
                      : nullptr;
-  T* dx = static_cast<T*>(g.dx.ptr) + row * g.dx.row + c;
-  T* dsi = g.dstate_in.ptr ? static_cast<T*>(g.dstate_in.ptr) + row * g.dstate_in.row + c : nullptr;
-  const int64_t set = row / d.rows_per_set;
-  float w[K][V], b[V], dw[K][V], db[V];
+  T* dx = static_cast<T*>(g.dx.ptr) + p.row * g.dx.row + p.c;
+  T* dsi = K > 1 && g.dstate_in.ptr ? static_cast<T*>(g.dstate_in.ptr) + p.row * g.dstate_in.row + p.c : nullptr;
+  auto dout_at = [&](int t) {
+    if (t < len) return load4<T, VEC>(dout + t * g.dout.step, p.have);
+    Vec<T, V> z;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    b[i] = a.bias.ptr ? a.bias.ptr[set * a.bias.stride + c + i] : 0.f;
-    db[i] = 0.f;
+    for (int i = 0; i < V; ++i) z.v[i] = from_f<T>(0.f);
+    return z;
+  };
+  float2 w[K][2], b[2], dw[K][2], db[2];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      w[k][i] = a.weight.ptr[set * a.weight.stride + (int64_t)k * d.D + c + i];
-      dw[k][i] = 0.f;
-    }
+  for (int k = 0; k < K; ++k) {
+    load_params(a.weight.ptr + p.set * a.weight.stride + (int64_t)k * d.D + p.c, p.have, d.params, w[k]);
+    zero(dw[k]);
   }
+  zero(b);
+  zero(db);
+  if (a.bias.ptr) load_params(a.bias.ptr + p.set * a.bias.stride + p.c, p.have, d.params, b);
   const bool silu = a.flags & ZO_CONV_SILU;
-  const int64_t t0 = (int64_t)run * d.run;
-  const int64_t t1 = t0 + d.run < d.T ? t0 + d.run : d.T;
-  // dx_p for p in [p0, p1): the first run begins with the carried window
-  const int64_t p0 = run == 0 ? -(K - 1) : t0, p1 = t1;
-  float xw[K - 1 + U][V], dd[K - 1 + U][V];  // x_{t-K+1..}, d_{t-K+1..}
+  const int t0 = p.run * d.run, t1 = t0 + d.run < d.T ? t0 + d.run : d.T;
+  const int p0 = p.run == 0 ? -(K - 1) : t0, last = t1 + K - 1;
+  Vec<T, V> nx[U], ny[U];
+#pragma unroll
+  for (int j = 0; j < U; ++j) nx[j] = in.at(t0 + j), ny[j] = dout_at(t0 + j);
+  float2 xw[K - 1 + U][2], dd[K - 1 + U][2];  // x_{t-K+1..}, d_{t-K+1..}
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
-    load_step<T, V, K>(x, a.x.step, s, a.state_in.step, t0 - (K - 1) + j, len, xw[j]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) dd[j][i] = 0.f;
+    pairs_of(in.at(t0 - (K - 1) + j), xw[j]);
+    zero(dd[j]);
   }
-  for (int64_t t = t0; t < t1 + K - 1; t += U) {
-    float dy[U][V];
+  for (int t = t0; t < last; t += U) {
+    float2 dy[U][2];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      load_step<T, V, K>(x, a.x.step, s, a.state_in.step, t + j, len, xw[K - 1 + j]);
-      if (t + j < len) {
-        load_vec<T, V>(dout + (t + j) * g.dout.step, dy[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) dy[j][i] = 0.f;
-      }
+      pairs_of(nx[j], xw[K - 1 + j]);
+      pairs_of(ny[j], dy[j]);
     }
+    if (t + U < last)
+#pragma unroll
+      for (int j = 0; j < U; ++j) nx[j] = in.at(t + U + j), ny[j] = dout_at(t + U + j);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const bool mine = t + j < t1, on = t + j < len;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float p = b[i];
+      for (int i = 0; i < 2; ++i) {
+        float2 v = dy[j][i];  // 0 behind the row's end
+        if (silu) {
+          float2 pre = b[i], s, slope;
 #pragma unroll
-        for (int k = 0; k < K; ++k) p = fmaf(w[k][i], xw[j + k][i], p);
-        const float v = on ? dy[j][i] * (silu ? dsilu_f(p) : 1.f) : 0.f;
+          for (int k = 0; k < K; ++k) pre = __ffma2_rn(w[k][i], xw[j + k][i], pre);
+          silu_slope_2(pre, s, slope);
+          v = t + j < len ? __fmul2_rn(v, slope) : two(0.f);
+        }
         dd[K - 1 + j][i] = v;
-        if (mine && on) {
-          db[i] += v;
+        if (t + j < t1) {
+          db[i] = __fadd2_rn(db[i], v);
 #pragma unroll
-          for (int k = 0; k < K; ++k) dw[k][i] = fmaf(v, xw[j + k][i], dw[k][i]);
+          for (int k = 0; k < K; ++k) dw[k][i] = __ffma2_rn(v, xw[j + k][i], dw[k][i]);
         }
       }
-      const int64_t p = t + j - (K - 1);
-      if (p >= p0 && p < p1) {
-        float o[V];
+      const int q = t + j - (K - 1);  // whose gradient is now complete
+      if (q >= p0 && q < t1) {
+        float2 o[2];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float v = 0.f;
+        for (int i = 0; i < 2; ++i) {
+          o[i] = two(0.f);
 #pragma unroll
-          for (int k = 0; k < K; ++k) v = fmaf(w[k][i], dd[j + K - 1 - k][i], v);
-          o[i] = v;
+          for (int k = 0; k < K; ++k) o[i] = __ffma2_rn(w[k][i], dd[j + K - 1 - k][i], o[i]);
         }
-        const int64_t q = p + K - 1 - len;  // which of the last inputs, if any
-        if (dso && q >= 0 && q < K - 1) {
-          float e[V];
-          load_vec<T, V>(dso + q * g.dstate_out.step, e);
-#pragma unroll
-          for (int i = 0; i < V; ++i) o[i] += e[i];
+        const int r = t + j - len;  // which of the last inputs, if any
+        if (dso && r >= 0 && r < K - 1) {
+          float2 e[2];
+          pairs_of(load4<T, VEC>(dso + r * g.dstate_out.step, p.have), e);
+          o[0] = __fadd2_rn(o[0], e[0]);
+          o[1] = __fadd2_rn(o[1], e[1]);
         }
-        if (p >= 0) {
-          store_vec<T, V>(dx + p * g.dx.step, o);
-        } else if (dsi) {
-          store_vec<T, V>(dsi + (p + K - 1) * g.dstate_in.step, o);
-        }
+        if (q >= 0)
+          store4<T, VEC>(dx + q * g.dx.step, p.have, o);
+        else if (dsi)
+          store4<T, VEC>(dsi + (q + K - 1) * g.dstate_in.step, p.have, o);
       }
     }
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
+      for (int j = 0; j < K - 1; ++j) {
         xw[j][i] = xw[U + j][i];
         dd[j][i] = dd[U + j][i];
       }
   }
   // partial sums of this run: [set][row of set, run][K + 1][D]
-  float* out = part + ((set * d.rows_per_set + row % d.rows_per_set) * d.runs + run) * (K + 1) * d.D + c;
+  float* out = part + (p.row * d.runs + p.run) * (K + 1) * d.D + p.c;
 #pragma unroll
-  for (int k = 0; k < K; ++k) store_vec<float, V>(out + (int64_t)k * d.D, dw[k]);
-  store_vec<float, V>(out + (int64_t)K * d.D, db);
+  for (int k = 0; k <= K; ++k) store4<float, VEC>(out + (int64_t)k * d.D, p.have, k < K ? dw[k < K ? k : K - 1] : db);
 }
 
 struct SumOuts {
@@ -264,48 +329,46 @@ __global__ void __launch_bounds__(32 * G)
   }
 }
 
-// Steps of one run: whole rows where there are rows enough for about eight
-// blocks an SM, else as many runs as give that, but not under 16 steps (and so
-// never under the K - 1 steps by which neighbouring runs overlap).
-ConvDims conv_dims(const zo_conv_args& a, int v) {
+// Steps of one run: whole rows where there are rows enough for `blocks` blocks an SM (two
+// waves of what stays there), else as many runs as give that, but not under 16 steps
+// (and so never under the K - 1 steps by which neighbouring runs overlap).  At most 256,
+// so that the backward pass's sums have two stages.
+ConvDims conv_dims(const zo_conv_args& a, int blocks) {
   ConvDims d;
   d.T = a.seq;
   d.D = a.channels;
   d.rows_per_set = a.rows / a.sets;
-  d.ctiles = (int)ceil_div(ceil_div(a.channels, v), kThreads);
-  const int64_t want = ceil_div(8 * kBlockSMs, (int64_t)d.ctiles * a.rows);
+  d.ctiles = (int)ceil_div(ceil_div(a.channels, V), kThreads);
+  const int64_t want = ceil_div(blocks * kBlockSMs, (int64_t)d.ctiles * a.rows);
   int64_t run = ceil_div(a.seq, want);
-  if (run < 16) run = 16;
+  run = run < 16 ? 16 : run > 256 ? 256 : run;
   d.run = (int)run;
   d.runs = (int)ceil_div(a.seq, run);
+  d.params = a.channels % V == 0;
+  for (const zo_f32* p : {&a.weight, &a.bias})
+    d.params = d.params && p->stride % V == 0 && reinterpret_cast<uintptr_t>(p->ptr) % 16 == 0;
   return d;
 }
+ConvDims forward_dims(const zo_conv_args& a) { return conv_dims(a, 10); }
+ConvDims backward_dims(const zo_conv_args& a) { return conv_dims(a, 8); }
 
-// As conv_dims for the backward pass, whose partial sums are laid out by run:
-// v = 1, so that the workspace does not go by alignment.
-ConvDims conv_backward_dims(const zo_conv_args& a, int v) {
-  ConvDims d = conv_dims(a, 4);
-  d.ctiles = (int)ceil_div(ceil_div(a.channels, v), kThreads);
-  return d;
-}
-
-template <class T, int V, int K>
+template <class T, int K, bool VEC>
 cudaError_t run_conv(const zo_conv_args& a, cudaStream_t st) {
-  const ConvDims d = conv_dims(a, V);
+  const ConvDims d = forward_dims(a);
   const int64_t blocks = (int64_t)d.ctiles * d.runs * a.rows;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  conv_kernel<T, V, K, 4><<<(unsigned)blocks, kThreads, 0, st>>>(a, d);
+  conv_kernel<T, K, 8, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(a, d);
   count_launch();
   return cudaGetLastError();
 }
 
-template <class T, int V, int K>
+template <class T, int K, bool VEC>
 cudaError_t run_conv_backward(const zo_conv_args& a, const zo_conv_grads& g, float* ws,
                               cudaStream_t st) {
-  const ConvDims d = conv_backward_dims(a, V);
+  const ConvDims d = backward_dims(a);
   const int64_t blocks = (int64_t)d.ctiles * d.runs * a.rows;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  conv_backward_kernel<T, V, K, 4><<<(unsigned)blocks, kThreads, 0, st>>>(a, g, d, ws);
+  conv_backward_kernel<T, K, 4, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(a, g, d, ws);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -313,50 +376,44 @@ cudaError_t run_conv_backward(const zo_conv_args& a, const zo_conv_grads& g, flo
   return launch_sum_parts(ws, a.sets, (int64_t)d.rows_per_set * d.runs, (int64_t)(K + 1) * d.D, outs, 2, st);
 }
 
-template <template <class, int, int> class F, class T, int V, class... A>
-cudaError_t by_taps(int taps, A&&... x) {
+template <class F>
+cudaError_t by_taps(int taps, F&& f) {
+  using std::integral_constant;
   switch (taps) {
-    case 1: return F<T, V, 1>::run(x...);
-    case 2: return F<T, V, 2>::run(x...);
-    case 3: return F<T, V, 3>::run(x...);
-    case 4: return F<T, V, 4>::run(x...);
-    case 5: return F<T, V, 5>::run(x...);
-    case 6: return F<T, V, 6>::run(x...);
-    case 7: return F<T, V, 7>::run(x...);
-    default: return F<T, V, 8>::run(x...);
+    case 1: return f(integral_constant<int, 1>());
+    case 2: return f(integral_constant<int, 2>());
+    case 3: return f(integral_constant<int, 3>());
+    case 4: return f(integral_constant<int, 4>());
+    case 5: return f(integral_constant<int, 5>());
+    case 6: return f(integral_constant<int, 6>());
+    case 7: return f(integral_constant<int, 7>());
+    default: return f(integral_constant<int, 8>());
   }
 }
 
-template <class T, int V, int K> struct Forward {
-  static cudaError_t run(const zo_conv_args& a, cudaStream_t st) { return run_conv<T, V, K>(a, st); }
-};
-template <class T, int V, int K> struct Backward {
-  static cudaError_t run(const zo_conv_args& a, const zo_conv_grads& g, float* ws, cudaStream_t st) {
-    return run_conv_backward<T, V, K>(a, g, ws, st);
-  }
-};
+// Whether four channels of all of these can be accessed together.
+bool vectors(std::initializer_list<const zo_tensor*> tensors, int elem, int channels) {
+  for (const zo_tensor* t : tensors)
+    if (vec_width(*t, elem, channels, V) != V) return false;
+  return true;
+}
 
 template <class T>
 cudaError_t conv_typed(const zo_conv_args& a, cudaStream_t st) {
-  constexpr int W = 16 / sizeof(T);
-  int v = W;
-  for (const zo_tensor* t : {&a.x, &a.out, &a.state_in, &a.state_out}) {
-    const int u = vec_width(*t, sizeof(T), a.channels, W);
-    v = u < v ? u : v;
-  }
-  return v == W ? by_taps<Forward, T, W>(a.taps, a, st) : by_taps<Forward, T, 1>(a.taps, a, st);
+  const bool vec = vectors({&a.x, &a.out, &a.state_in, &a.state_out}, sizeof(T), a.channels);
+  return by_taps(a.taps, [&](auto k) {
+    return vec ? run_conv<T, decltype(k)::value, true>(a, st) : run_conv<T, decltype(k)::value, false>(a, st);
+  });
 }
 
 template <class T>
 cudaError_t conv_backward_typed(const zo_conv_args& a, const zo_conv_grads& g, float* ws,
                                 cudaStream_t st) {
-  int v = 4;
-  for (const zo_tensor* t : {&a.x, &a.state_in, &g.dout, &g.dx, &g.dstate_out, &g.dstate_in}) {
-    const int u = vec_width(*t, sizeof(T), a.channels, 4);
-    v = u < v ? u : v;
-  }
-  return v == 4 ? by_taps<Backward, T, 4>(a.taps, a, g, ws, st)
-                : by_taps<Backward, T, 1>(a.taps, a, g, ws, st);
+  const bool vec = vectors({&a.x, &a.state_in, &g.dout, &g.dx, &g.dstate_out, &g.dstate_in}, sizeof(T), a.channels);
+  return by_taps(a.taps, [&](auto k) {
+    return vec ? run_conv_backward<T, decltype(k)::value, true>(a, g, ws, st)
+               : run_conv_backward<T, decltype(k)::value, false>(a, g, ws, st);
+  });
 }
 
 }  // namespace
@@ -395,7 +452,7 @@ cudaError_t launch_conv(const zo_conv_args& a, cudaStream_t st) {
 }
 
 int64_t conv_backward_workspace(const zo_conv_args& a) {
-  const ConvDims d = conv_backward_dims(a, 1);
+  const ConvDims d = backward_dims(a);
   return (int64_t)a.rows * d.runs * (a.taps + 1) * a.channels * (int64_t)sizeof(float);
 }
 

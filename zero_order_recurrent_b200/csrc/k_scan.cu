@@ -34,24 +34,6 @@ __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t ro
   return n < 0 ? 0 : T;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLog2eLow = 1.92596299e-8f;  // log2(e) - kLog2e
-constexpr float kLn2 = 0.69314718055994531f;
-
-__device__ __forceinline__ float exp2_1(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_1(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 exp2_2(float2 x) { return make_float2(exp2_1(x.x), exp2_1(x.y)); }
-__device__ __forceinline__ float2 rcp_2(float2 x) { return make_float2(rcp_1(x.x), rcp_1(x.y)); }
-
 // 2^x, more exactly for |x| < 1/16: the special function unit's results there are too small by
 // 1e-7 of themselves on average (they are cut off, measured), which over the 1 / |x| steps
 // that such a decay lasts adds up to 1e-6 of a state.  A polynomial of degree 3, 1 at 0, with the least largest relative error up to 1/16
@@ -96,12 +78,6 @@ __device__ __forceinline__ float2 softplus_2(float2 x) {
   return __fadd2_rn(make_float2(relu_nan(x.x), relu_nan(x.y)), l);
 }
 __device__ __forceinline__ float softplus_f(float x) { return softplus_2(two(x)).x; }
-
-// x sigmoid(x)
-__device__ __forceinline__ float2 silu_2(float2 x) {
-  const float2 e = exp2_2(__fmul2_rn(x, two(-kLog2e)));
-  return __fmul2_rn(x, rcp_2(__fadd2_rn(e, two(1.f))));
-}
 
 template <int LN>
 __device__ __forceinline__ float sum_lanes(float v) {
@@ -897,13 +873,12 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
         float2 dt = raw, slope = two(1.f), dy = make_float2(fo[e], fo[e + 1]), zf = two(0.f);
         if (softplus) {
           dt = softplus_2(raw);
-          slope = rcp_2(__fadd2_rn(exp2_2(__fmul2_rn(raw, two(-kLog2e))), two(1.f)));
+          slope = sigmoid_2(raw);
         }
         if (gate) {
-          const float2 z = make_float2(fz[e], fz[e + 1]);
-          const float2 r = rcp_2(__fadd2_rn(exp2_2(__fmul2_rn(z, two(-kLog2e))), two(1.f)));
-          const float2 v = __fmul2_rn(z, r);  // silu
-          zf = __fmul2_rn(dy, __ffma2_rn(v, __ffma2_rn(r, two(-1.f), two(1.f)), r));
+          float2 v;  // silu(z)
+          silu_slope_2(make_float2(fz[e], fz[e + 1]), v, zf);
+          zf = __fmul2_rn(dy, zf);
           dy = __fmul2_rn(dy, v);
         }
         const bool in = t < end;

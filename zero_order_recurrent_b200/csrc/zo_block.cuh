@@ -41,12 +41,63 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
   *reinterpret_cast<Vec<T, V>*>(p) = x;
 }
 
-__device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
-__device__ __forceinline__ float silu_f(float x) { return x / (1.f + expf(-x)); }
-// d silu / dx = q (1 + x (1 - q)), q = sigmoid(x)
-__device__ __forceinline__ float dsilu_f(float x) {
-  const float q = sigmoid_f(x);
-  return q * (1.f + x * (1.f - q));
+// A load that does not stay in the first-level cache: for data read once.
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> load_streaming(const Vec<T, V>* p) {
+  constexpr int B = sizeof(T) * V;
+  union {
+    Vec<T, V> x;
+    uint4 q[B < 16 ? 1 : B / 16];
+    uint2 d;
+    unsigned w;
+    unsigned short h;
+  } u;
+  if constexpr (B >= 16) {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(u.q[i].x), "=r"(u.q[i].y), "=r"(u.q[i].z), "=r"(u.q[i].w)
+                   : "l"(reinterpret_cast<const uint4*>(p) + i));
+  } else if constexpr (B == 8) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(u.d.x), "=r"(u.d.y) : "l"(p));
+  } else if constexpr (B == 4) {
+    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(u.w) : "l"(p));
+  } else {
+    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(u.h) : "l"(p));
+  }
+  return u.x;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLow = 1.92596299e-8f;  // log2(e) - kLog2e
+constexpr float kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ float exp2_1(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_1(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 exp2_2(float2 x) { return make_float2(exp2_1(x.x), exp2_1(x.y)); }
+__device__ __forceinline__ float2 rcp_2(float2 x) { return make_float2(rcp_1(x.x), rcp_1(x.y)); }
+
+// sigmoid(x); e^-x from a product rounded once, so off by |x| 2^-24 of itself and a few
+// units in the last place
+__device__ __forceinline__ float2 sigmoid_2(float2 x) {
+  return rcp_2(__fadd2_rn(exp2_2(__fmul2_rn(x, two(-kLog2e))), two(1.f)));
+}
+__device__ __forceinline__ float2 silu_2(float2 x) { return __fmul2_rn(x, sigmoid_2(x)); }
+
+// silu(x) = x q and its slope q (1 + x (1 - q)), q = sigmoid(x)
+__device__ __forceinline__ void silu_slope_2(float2 x, float2& v, float2& slope) {
+  const float2 q = sigmoid_2(x);
+  v = __fmul2_rn(x, q);
+  slope = __ffma2_rn(v, __ffma2_rn(q, two(-1.f), two(1.f)), q);
 }
 
 }  // namespace zo
