@@ -34,15 +34,16 @@ __device__ __forceinline__ int row_length(const int32_t* lengths, int64_t row, i
   return n < 0 ? 0 : T;
 }
 
-// Four channels from p, of which `have` exist (VEC: always all, on a vector's boundary).
+// Four channels from p, of which `have` exist (VEC: always all, on a vector's boundary); zeros
+// where `on` is false.
 template <class T, bool VEC>
-__device__ __forceinline__ Vec<T, V> load4(const T* p, int have) {
+__device__ __forceinline__ Vec<T, V> load4(const T* p, int have, bool on) {
   if constexpr (VEC) {
-    return *reinterpret_cast<const Vec<T, V>*>(p);
+    return load_if<T, V>(p, on);
   } else {
     Vec<T, V> x;
 #pragma unroll
-    for (int i = 0; i < V; ++i) x.v[i] = i < have ? p[i] : from_f<T>(0.f);
+    for (int i = 0; i < V; ++i) x.v[i] = load_if<T, 1>(p + i, on && i < have).v[0];
     return x;
   }
 }
@@ -110,13 +111,12 @@ struct Inputs {
     len = n;
     have = p.have;
   }
-  __device__ __forceinline__ Vec<T, V> at(int t) const {
-    if (t >= 0 && t < len) return load4<T, VEC>(x + t * x_step, have);
-    if (t < 0 && s) return load4<T, VEC>(s + (t + K - 1) * s_step, have);
-    Vec<T, V> z;
-#pragma unroll
-    for (int i = 0; i < V; ++i) z.v[i] = from_f<T>(0.f);
-    return z;
+  __device__ __forceinline__ Vec<T, V> at(int t) const {  // any step
+    const T* p = t >= 0 ? x + t * x_step : s + (t + K - 1) * s_step;
+    return load4<T, VEC>(p, have, t >= 0 ? t < len : s != nullptr);
+  }
+  __device__ __forceinline__ Vec<T, V> from_x(int t) const {  // t >= 0
+    return load4<T, VEC>(x + t * x_step, have, t < len);
   }
 };
 
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(zo_conv_args a, ConvDims
   const int t0 = p.run * d.run, t1 = t0 + d.run < d.T ? t0 + d.run : d.T;
   Vec<T, V> next[U];
 #pragma unroll
-  for (int j = 0; j < U; ++j) next[j] = in.at(t0 + j);
+  for (int j = 0; j < U; ++j) next[j] = in.from_x(t0 + j);
   float2 win[K - 1 + U][2];
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) pairs_of(in.at(t0 - (K - 1) + j), win[j]);
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(zo_conv_args a, ConvDims
     for (int j = 0; j < U; ++j) pairs_of(next[j], win[K - 1 + j]);
     if (t + U < t1)
 #pragma unroll
-      for (int j = 0; j < U; ++j) next[j] = in.at(t + U + j);
+      for (int j = 0; j < U; ++j) next[j] = in.from_x(t + U + j);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (t + j >= t1) break;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(zo_conv_args a, ConvDims
 // The run of steps [t0, t1) owns d_t for the sums, and gives dx_p for p in [t0, t1);
 // the first run also for p < 0, which is the carried window's gradient.
 template <class T, int K, int U, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, K <= 4 ? 4 : K <= 5 ? 3 : 2)
     conv_backward_kernel(zo_conv_args a, zo_conv_grads g, ConvDims d, float* part) {
   const Place p = place(d);
   if (p.have <= 0) return;
@@ -195,13 +195,7 @@ __global__ void __launch_bounds__(kThreads)
                      : nullptr;
   T* dx = static_cast<T*>(g.dx.ptr) + p.row * g.dx.row + p.c;
   T* dsi = K > 1 && g.dstate_in.ptr ? static_cast<T*>(g.dstate_in.ptr) + p.row * g.dstate_in.row + p.c : nullptr;
-  auto dout_at = [&](int t) {
-    if (t < len) return load4<T, VEC>(dout + t * g.dout.step, p.have);
-    Vec<T, V> z;
-#pragma unroll
-    for (int i = 0; i < V; ++i) z.v[i] = from_f<T>(0.f);
-    return z;
-  };
+  auto dout_at = [&](int t) { return load4<T, VEC>(dout + t * g.dout.step, p.have, t < len); };
   float2 w[K][2], b[2], dw[K][2], db[2];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -216,7 +210,7 @@ __global__ void __launch_bounds__(kThreads)
   const int p0 = p.run == 0 ? -(K - 1) : t0, last = t1 + K - 1;
   Vec<T, V> nx[U], ny[U];
 #pragma unroll
-  for (int j = 0; j < U; ++j) nx[j] = in.at(t0 + j), ny[j] = dout_at(t0 + j);
+  for (int j = 0; j < U; ++j) nx[j] = in.from_x(t0 + j), ny[j] = dout_at(t0 + j);
   float2 xw[K - 1 + U][2], dd[K - 1 + U][2];  // x_{t-K+1..}, d_{t-K+1..}
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
@@ -232,7 +226,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (t + U < last)
 #pragma unroll
-      for (int j = 0; j < U; ++j) nx[j] = in.at(t + U + j), ny[j] = dout_at(t + U + j);
+      for (int j = 0; j < U; ++j) nx[j] = in.from_x(t + U + j), ny[j] = dout_at(t + U + j);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
 #pragma unroll
@@ -264,7 +258,7 @@ __global__ void __launch_bounds__(kThreads)
         const int r = t + j - len;  // which of the last inputs, if any
         if (dso && r >= 0 && r < K - 1) {
           float2 e[2];
-          pairs_of(load4<T, VEC>(dso + r * g.dstate_out.step, p.have), e);
+          pairs_of(load4<T, VEC>(dso + r * g.dstate_out.step, p.have, true), e);
           o[0] = __fadd2_rn(o[0], e[0]);
           o[1] = __fadd2_rn(o[1], e[1]);
         }

@@ -59,14 +59,7 @@ struct Share {
   template <class T>
   __device__ __forceinline__ void load(const T* row, Vec<T, V> (&x)[E]) const {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (has(e)) {
-        x[e] = load_streaming(reinterpret_cast<const Vec<T, V>*>(row + channel(e)));
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[e].v[v] = from_f<T>(0.f);
-      }
-    }
+    for (int e = 0; e < E; ++e) x[e] = load_if<T, V>(row + channel(e), has(e));
   }
   template <class T>
   __device__ __forceinline__ static void floats(const Vec<T, V> (&x)[E], float (&f)[N]) {
@@ -189,7 +182,7 @@ __global__ void __launch_bounds__(block_of<W>())
 // rows) the sums are in shared memory, each thread's its own, and the parameters are loaded
 // again from the first-level cache.
 template <class T, class XT, int V, int E, int W>
-__global__ void __launch_bounds__(block_of<W>(), 1)
+__global__ void __launch_bounds__(block_of<W>(), V * E <= 8 ? 512 / block_of<W>() : 1)
     norm_backward_kernel(zo_norm_args a, zo_norm_grads g, int rows_per_set, int groups, bool pvec, float* part) {
   constexpr int kRows = block_of<W>() / W;  // groups of a block
   __shared__ float sh[3 * (block_of<W>() / 32)];

@@ -41,10 +41,13 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
   *reinterpret_cast<Vec<T, V>*>(p) = x;
 }
 
-// A load that does not stay in the first-level cache: for data read once.
+// V values from p, or zeros where `on` is false.  One predicated instruction: a branch
+// around a load lets the compiler pull the conversion of its result in too, and then every
+// load waits for the one before it.  The data is read once and does not stay in the first-level
+// cache.
 template <class T, int V>
-__device__ __forceinline__ Vec<T, V> load_streaming(const Vec<T, V>* p) {
-  constexpr int B = sizeof(T) * V;
+__device__ __forceinline__ Vec<T, V> load_if(const T* p, bool on) {
+  constexpr int B = (int)sizeof(T) * V;
   union {
     Vec<T, V> x;
     uint4 q[B < 16 ? 1 : B / 16];
@@ -55,15 +58,25 @@ __device__ __forceinline__ Vec<T, V> load_streaming(const Vec<T, V>* p) {
   if constexpr (B >= 16) {
 #pragma unroll
     for (int i = 0; i < B / 16; ++i)
-      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(u.q[i].x), "=r"(u.q[i].y), "=r"(u.q[i].z), "=r"(u.q[i].w)
-                   : "l"(reinterpret_cast<const uint4*>(p) + i));
+      asm volatile(
+          "{.reg .pred q; setp.ne.u32 q, %5, 0; mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0; "
+          "@q ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];}"
+          : "=&r"(u.q[i].x), "=&r"(u.q[i].y), "=&r"(u.q[i].z), "=&r"(u.q[i].w)
+          : "l"(reinterpret_cast<const uint4*>(p) + i), "r"((unsigned)on));
   } else if constexpr (B == 8) {
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(u.d.x), "=r"(u.d.y) : "l"(p));
+    asm volatile(
+        "{.reg .pred q; setp.ne.u32 q, %3, 0; mov.b32 %0, 0; mov.b32 %1, 0; "
+        "@q ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];}"
+        : "=&r"(u.d.x), "=&r"(u.d.y)
+        : "l"(p), "r"((unsigned)on));
   } else if constexpr (B == 4) {
-    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(u.w) : "l"(p));
+    asm volatile("{.reg .pred q; setp.ne.u32 q, %2, 0; mov.b32 %0, 0; @q ld.global.L1::no_allocate.u32 %0, [%1];}"
+                 : "=&r"(u.w)
+                 : "l"(p), "r"((unsigned)on));
   } else {
-    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(u.h) : "l"(p));
+    asm volatile("{.reg .pred q; setp.ne.u32 q, %2, 0; mov.b16 %0, 0; @q ld.global.L1::no_allocate.u16 %0, [%1];}"
+                 : "=&h"(u.h)
+                 : "l"(p), "r"((unsigned)on));
   }
   return u.x;
 }
