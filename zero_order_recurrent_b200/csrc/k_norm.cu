@@ -57,9 +57,10 @@ struct Share {
   __device__ __forceinline__ bool has(int e) const { return channel(e) < D; }  // V divides D
 
   template <class T>
-  __device__ __forceinline__ void load(const T* row, Vec<T, V> (&x)[E]) const {
+  __device__ __forceinline__ void load(const zo_tensor& t, int64_t row, Vec<T, V> (&x)[E]) const {
+    const T* p = static_cast<const T*>(t.ptr) + row * t.row;  // zeros where there is no tensor
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = load_if<T, V>(row + channel(e), has(e));
+    for (int e = 0; e < E; ++e) x[e] = load_if<T, V>(p + channel(e), t.ptr && has(e));
   }
   template <class T>
   __device__ __forceinline__ static void floats(const Vec<T, V> (&x)[E], float (&f)[N]) {
@@ -130,9 +131,9 @@ __global__ void __launch_bounds__(block_of<W>())
   const bool first = a.flags & ZO_NORM_GATE_FIRST, block = a.o.ptr, gate = a.gate.ptr;
   Vec<XT, V> rx[E];
   Vec<T, V> ro[E], rg[E];
-  me.load(static_cast<const XT*>(a.x.ptr) + row * a.x.row, rx);
-  if (block) me.load(static_cast<const T*>(a.o.ptr) + row * a.o.row, ro);
-  if (gate) me.load(static_cast<const T*>(a.gate.ptr) + row * a.gate.row, rg);
+  me.load(a.x, row, rx);
+  me.load(a.o, row, ro);
+  me.load(a.gate, row, rg);
   float x[N];
   S::floats(rx, x);
   if (block) {
@@ -225,11 +226,11 @@ __global__ void __launch_bounds__(block_of<W>(), V * E <= 8 ? 512 / block_of<W>(
     const int64_t row = (int64_t)set * rows_per_set + (on ? k : rows_per_set - 1);
     Vec<XT, V> ry[E], rG[E];
     Vec<T, V> ro[E], rz[E], rn_[E];
-    me.load(static_cast<const XT*>(a.x_out.ptr) + row * a.x_out.row, ry);
-    if (g.dx_out.ptr) me.load(static_cast<const XT*>(g.dx_out.ptr) + row * g.dx_out.row, rG);
-    if (next) me.load(static_cast<const T*>(g.dn.ptr) + row * g.dn.row, rn_);
-    if (block) me.load(static_cast<const T*>(a.o.ptr) + row * a.o.row, ro);
-    if (gate) me.load(static_cast<const T*>(a.gate.ptr) + row * a.gate.row, rz);
+    me.load(a.x_out, row, ry);
+    me.load(g.dx_out, row, rG);
+    me.load(g.dn, row, rn_);
+    me.load(a.o, row, ro);
+    me.load(a.gate, row, rz);
     // v and, where there is a gate, its activation and slope, for channels i, i + 1 of a thread
     // (pairs reach across vectors where those have one channel)
     auto pair = [&](const auto& x, int i) {
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(block_of<W>(), V * E <= 8 ? 512 / block_of<W>(
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int i = e * V + v;
-        G[i] = g.dx_out.ptr ? to_f(rG[e].v[v]) : 0.f;
+        G[i] = to_f(rG[e].v[v]);
         if (next) {
           const float y = to_f(ry[e].v[v]), dn = to_f(rn_[e].v[v]);
           if (on) add(s_pre, 0, i, dn * (y * rn));
@@ -386,13 +387,15 @@ int backward_width(int channels) {
          : channels <= 8192 ? 512 : 1024;
 }
 
-// Row groups of one set in the backward pass (a multiple of 4, the most that a
-// block holds): about 512 threads an SM, and no more groups than rows.
+// Row groups of one set in the backward pass: no more than fill the SMs once, at 512 threads an
+// SM, nor more than there are rows; a multiple of those that a block holds.
 int norm_groups(const zo_norm_args& a) {
-  int64_t g = ceil_div((int64_t)kBlockSMs * 512 / backward_width(a.channels), a.sets);
+  const int w = backward_width(a.channels), held = w < 128 ? 128 / w : 1;
+  int64_t g = (int64_t)kBlockSMs * 512 / w / a.sets;
   const int64_t rows = a.rows / a.sets;
-  if (g > rows) g = rows;
-  return (int)(ceil_div(g, 4) * 4);
+  if (g > rows) g = ceil_div(rows, held) * held;
+  g = g / held * held;
+  return (int)(g < held ? held : g);
 }
 
 // Whether a parameter's rows start on 16 bytes.

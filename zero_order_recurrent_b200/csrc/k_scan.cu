@@ -842,38 +842,28 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
   int chunks = 0;
   for (int t0 = end > tb ? tb + (end - 1 - tb) / kChunk * kChunk : tb - 1; t0 >= tb; t0 -= kChunk) {
     __syncthreads();
-    // The chunk's inputs and what is one channel's and step's, four channels at a time; the
-    // loads of all steps first.
-    constexpr int kSteps = S::kThreads / kQuads, kLoads = (kChunk + kSteps - 1) / kSteps;
-    Vec<T, 4> ru[kLoads], rd[kLoads], ro[kLoads], rz[kLoads];
-    auto load_quad = [&](const T* p, bool on) {
-      if (vec) return load_if<T, 4>(p, on && pc < left);
-      Vec<T, 4> x;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x.v[e] = load_if<T, 1>(p + e, on && pc + e < left).v[0];
-      return x;
-    };
-#pragma unroll
-    for (int l = 0; l < kLoads; ++l) {
-      const int64_t t = t0 + tid / kQuads + l * kSteps;
-      const bool on = t < end;
-      ru[l] = load_quad(bu + t * a.u.step + pc, on);
-      rd[l] = load_quad(bd + t * a.delta.step + pc, on);
-      ro[l] = load_quad(bo + t * g.dout.step + pc, on);
-      if (gate) rz[l] = load_quad(bz + t * a.z.step + pc, on);
-    }
-#pragma unroll
-    for (int l = 0; l < kLoads; ++l) {
-      const int s = tid / kQuads + l * kSteps, c = pc;
-      if (kSteps > kChunk && s >= kChunk) break;
+    // The chunk's inputs and what is one channel's and step's, four channels at a time.
+#pragma unroll 2
+    for (int s = tid / kQuads; s < kChunk; s += S::kThreads / kQuads) {
+      const int c = pc;
       const int64_t t = t0 + s;
-      float fu[4], fd[4], fz[4], fo[4];
+      float fu[4] = {}, fd[4] = {}, fz[4] = {}, fo[4] = {};
+      if (t < end) {
+        if (vec && c < left) {
+          load_vec<T, 4>(bu + t * a.u.step + c, fu);
+          load_vec<T, 4>(bd + t * a.delta.step + c, fd);
+          load_vec<T, 4>(bo + t * g.dout.step + c, fo);
+          if (gate) load_vec<T, 4>(bz + t * a.z.step + c, fz);
+        } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        fu[e] = to_f(ru[l].v[e]);
-        fd[e] = to_f(rd[l].v[e]);
-        fo[e] = to_f(ro[l].v[e]);
-        fz[e] = gate ? to_f(rz[l].v[e]) : 0.f;
+          for (int e = 0; e < 4; ++e)
+            if (c + e < left) {
+              fu[e] = to_f(bu[t * a.u.step + c + e]);
+              fd[e] = to_f(bd[t * a.delta.step + c + e]);
+              fo[e] = to_f(bo[t * g.dout.step + c + e]);
+              if (gate) fz[e] = to_f(bz[t * a.z.step + c + e]);
+            }
+        }
       }
       float o[5][4];
 #pragma unroll
