@@ -16,8 +16,9 @@ Where `workspace` is not given, it comes from torch's allocator for this call.
 from __future__ import annotations
 
 import ctypes
+import struct
 
-from . import ZO_DTYPE_BF16, ZO_DTYPE_FP32, ZO_ERR_INVALID_ARG, ZOError, _check, load_library
+from . import ZO_DTYPE_BF16, ZO_DTYPE_FP32, _check, load_library
 
 ZO_DTYPE_FP16 = 2
 ZO_MAX_TAPS = 8
@@ -98,7 +99,6 @@ def declare(lib):
         f.restype = res
 
 
-_NO_TENSOR, _NO_F32 = _Tensor(), _F32()
 torch = None   # imported by the first call, as by the package's other calls
 _DTYPES = {}
 
@@ -110,8 +110,30 @@ def _import_torch():
                     torch.float16: ZO_DTYPE_FP16})
 
 
+def _packer(structure):
+    """struct.Struct with the layout of a ctypes Structure, its parts spelled out flat: packing
+    one is several times quicker than filling the nested fields of the other."""
+    code = {_I32: "i", ctypes.c_float: "f", _P: "P", _I64: "q"}
+
+    def flat(s):
+        for _, t in s._fields_:
+            if hasattr(t, "_fields_"):
+                yield from flat(t)
+            else:
+                yield code[t]
+    p = struct.Struct("@" + "".join(flat(structure)))
+    assert p.size == ctypes.sizeof(structure)
+    return p.pack
+
+
+_PACK = {t: _packer(t) for t in (ConvArgs, ConvGrads, ScanArgs, ScanGrads, NormArgs, NormGrads)}
+_CALLS = {}  # the library's functions, taking packed structures
+_NONE2, _NONE3 = (0, 0), (0, 0, 0)
+
+
 class _Call:
-    """The tensors of one call: checks them against the first one's device."""
+    """The tensors of one call: checks them against the first one's device.  act, param, grad and
+    states give a tensor's fields of the C structures."""
 
     def __init__(self, where, first):
         if torch is None:
@@ -119,15 +141,15 @@ class _Call:
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise ValueError(f"{where}: CUDA tensors are required")
         self.where = where
-        self.device = first.device
+        self.index = first.get_device()
 
     def fail(self, name, what):
         raise ValueError(f"{self.where}: {name} {what}")
 
     def check(self, name, t, dtype):
-        if not isinstance(t, torch.Tensor) or t.device != self.device:
-            self.fail(name, f"must be a tensor on {self.device}")
-        if t.dtype != dtype:
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
+            self.fail(name, f"must be a tensor on cuda:{self.index}")
+        if t.dtype is not dtype:
             self.fail(name, f"must be {dtype}, got {t.dtype}")
 
     def code(self, t):
@@ -138,65 +160,68 @@ class _Call:
         return c
 
     def act(self, name, t, shape, dtype, optional=False, inner=1):
-        """A _Tensor of this shape: rows, steps or none, and `inner` contiguous dimensions."""
+        """A tensor of this shape: rows, steps or none, and `inner` contiguous dimensions."""
         if t is None and optional:
-            return _NO_TENSOR
+            return _NONE3
         self.check(name, t, dtype)
         if t.shape != shape:
             self.fail(name, f"must have shape {tuple(shape)}, got {tuple(t.shape)}")
         st = t.stride()
-        if shape[-1] != 1 and st[-1] != 1:
+        if st[-1] != 1 and shape[-1] != 1:
             self.fail(name, "must be contiguous in its last dimension")
-        if inner == 2 and shape[-2] != 1 and st[-2] != shape[-1]:
+        if inner == 2 and st[-2] != shape[-1] and shape[-2] != 1:
             self.fail(name, "must be contiguous in its last two dimensions")
-        return _Tensor(t.data_ptr(), st[0], st[1] if len(shape) - inner == 2 else 0)
+        return t.data_ptr(), st[0], st[1] if len(st) - inner == 2 else 0
 
     def param(self, name, t, inner, sets, optional=False):
-        """An _F32 of parameters [inner] or [sets, inner]."""
+        """Parameters [inner] or [sets, inner]."""
         if t is None and optional:
-            return _NO_F32
+            return _NONE2
         self.check(name, t, torch.float32)
-        n = len(inner)
-        if t.shape[-n:] != inner or t.dim() not in (n, n + 1):
-            self.fail(name, f"must have shape {tuple(inner)} or [sets, ...], got {tuple(t.shape)}")
-        self.contiguous(name, t, n)
-        if t.dim() == n or t.shape[0] == 1:
-            return _F32(t.data_ptr(), 0)
-        if t.shape[0] != sets:
-            self.fail(name, f"has {t.shape[0]} sets, others {sets}")
-        return _F32(t.data_ptr(), t.stride(0))
+        n, shape = len(inner), t.shape
+        if shape[-n:] != inner or len(shape) - n not in (0, 1):
+            self.fail(name, f"must have shape {tuple(inner)} or [sets, ...], got {tuple(shape)}")
+        st = self.contiguous(name, t, n)
+        if len(shape) == n or shape[0] == 1:
+            return t.data_ptr(), 0
+        if shape[0] != sets:
+            self.fail(name, f"has {shape[0]} sets, others {sets}")
+        return t.data_ptr(), st[0]
 
     def contiguous(self, name, t, n):
-        want = 1
-        for size, stride in zip(reversed(t.shape[-n:]), reversed(t.stride()[-n:])):
-            if size != 1 and stride != want:
-                self.fail(name, f"must be contiguous in its last {n} dimensions")
-            want *= size
+        """The strides of a tensor whose last n dimensions are contiguous."""
+        st = t.stride()
+        if not t.is_contiguous():
+            want = 1
+            for size, stride in zip(reversed(t.shape[-n:]), reversed(st[-n:])):
+                if size != 1 and stride != want:
+                    self.fail(name, f"must be contiguous in its last {n} dimensions")
+                want *= size
+        return st
 
     def grad(self, name, t, inner, sets, optional=False):
-        """An _F32 of parameter gradients: one for each set."""
+        """Parameter gradients: one for each set."""
         if t is None and optional:
-            return _NO_F32
+            return _NONE2
         self.check(name, t, torch.float32)
         n = len(inner)
         if not (t.shape == (sets, *inner) or (sets == 1 and t.shape == inner)):
             self.fail(name, f"must have shape {(sets, *inner)}, got {tuple(t.shape)}")
-        self.contiguous(name, t, n)
-        return _F32(t.data_ptr(), t.stride(0) if t.dim() > n else 0)
+        st = self.contiguous(name, t, n)
+        return t.data_ptr(), st[0] if len(st) > n else 0
 
     def states(self, name, t, shape, optional=True):
-        """An _F32 of recurrent states [rows, channels, states]."""
+        """Recurrent states [rows, channels, states]."""
         if t is None and optional:
-            return _NO_F32
+            return _NONE2
         self.check(name, t, torch.float32)
         if t.shape != shape:
             self.fail(name, f"must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        self.contiguous(name, t, 2)
-        return _F32(t.data_ptr(), t.stride(0))
+        return t.data_ptr(), self.contiguous(name, t, 2)[0]
 
     def ints(self, name, t, n):
         if t is None:
-            return None
+            return 0
         self.check(name, t, torch.int32)
         if t.shape != (n,) or (n != 1 and t.stride(0) != 1):
             self.fail(name, f"must be contiguous of shape {(n,)}")
@@ -205,36 +230,47 @@ class _Call:
     def run(self, name, *args, stream=None, workspace=None):
         """Calls `name` on the tensors' device.  workspace: None for a call without
         one, else (the caller's tensor or None, bytes)."""
-        lib = load_library()
-        cur = torch.cuda.current_stream(self.device)
-        handle = cur.cuda_stream
+        cur = torch.cuda.current_stream(self.index)
+        handle = current = cur.cuda_stream
         if stream is not None:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
         if workspace is not None:
             ws, need = workspace
             if need < 0:
-                raise ZOError(ZO_ERR_INVALID_ARG, name)
-            if ws is None and need:
-                ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-                if handle != cur.cuda_stream:
-                    # the allocator would hand it out again on the current stream
-                    other = stream if not isinstance(stream, int) else \
-                        torch.cuda.ExternalStream(stream, device=self.device)
-                    other.wait_stream(cur)
-                    ws.record_stream(other)
-            elif ws is not None:
-                if not isinstance(ws, torch.Tensor) or ws.device != self.device or \
+                # the sizes are refused: the call itself says why
+                args += (None, 0)
+            elif ws is None:
+                if need:
+                    ws = torch.empty(need, dtype=torch.uint8, device=f"cuda:{self.index}")
+                    if handle != current:
+                        # the allocator would hand it out again on the current stream
+                        other = stream if not isinstance(stream, int) else \
+                            torch.cuda.ExternalStream(stream, device=self.index)
+                        other.wait_stream(cur)
+                        ws.record_stream(other)
+                args += (ws.data_ptr() if need else None, need)
+            else:
+                if not isinstance(ws, torch.Tensor) or ws.get_device() != self.index or \
                         not ws.is_contiguous():
-                    self.fail("workspace", f"must be a contiguous tensor on {self.device}")
-            args += (ws.data_ptr() if ws is not None else None,
-                     ws.numel() * ws.element_size() if ws is not None else 0)
-        f = getattr(lib, name)
-        if torch.cuda.current_device() == self.device.index:
+                    self.fail("workspace", f"must be a contiguous tensor on cuda:{self.index}")
+                args += (ws.data_ptr(), ws.numel() * ws.element_size())
+        f = _call(name)
+        if torch.cuda.current_device() == self.index:
             st = f(*args, handle)
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(self.index):
                 st = f(*args, handle)
-        _check(st, name)
+        if st:
+            _check(st, name)
+
+
+def _call(name):
+    f = _CALLS.get(name)
+    if f is None:
+        of = getattr(load_library(), name)
+        types = [_P if hasattr(t, "contents") else t for t in of.argtypes]
+        f = _CALLS[name] = ctypes.CFUNCTYPE(of.restype, *types)((name, load_library()))
+    return f
 
 
 def _sets(*pairs):
@@ -258,12 +294,12 @@ def _conv_args(c, x, weight, out, bias, silu, lengths, state_in, state_out, stat
     S = _sets((weight, 2), (bias, 1))
     win = (R, K - 1, D)
     # a window of one tap holds nothing
-    st = [_NO_TENSOR if K == 1 else c.act(n, t, win, dt, True)
+    st = [_NONE3 if K == 1 else c.act(n, t, win, dt, True)
           for n, t in (("state_in", state_in), ("state_out", state_out))]
-    return ConvArgs(
-        R, T, D, K, S, c.code(x), ZO_CONV_SILU if silu else 0, c.act("x", x, x.shape, dt),
-        c.act("out", out, x.shape, dt, True), c.param("weight", weight, (K, D), S),
-        c.param("bias", bias, (D,), S, True), c.ints("lengths", lengths, R), st[0], st[1],
+    return (K, S), _PACK[ConvArgs](
+        R, T, D, K, S, c.code(x), ZO_CONV_SILU if silu else 0, *c.act("x", x, x.shape, dt),
+        *c.act("out", out, x.shape, dt, True), *c.param("weight", weight, (K, D), S),
+        *c.param("bias", bias, (D,), S, True), c.ints("lengths", lengths, R), *st[0], *st[1],
         c.ints("status", status, 1))
 
 
@@ -277,7 +313,7 @@ def zo_conv(x, weight, out, bias=None, silu=True, lengths=None, state_in=None, s
     c = _Call("zo_conv", x)
     if x.dim() != 3:
         c.fail("x", "must be [rows, seq, channels]")
-    a = _conv_args(c, x, weight, out, bias, silu, lengths, state_in, state_out, status)
+    _, a = _conv_args(c, x, weight, out, bias, silu, lengths, state_in, state_out, status)
     c.run("zo_conv", a, stream=stream)
 
 
@@ -288,8 +324,8 @@ def zo_conv_step(x, weight, state, out, bias=None, silu=True, state_out=None, st
     c = _Call("zo_conv_step", x)
     if x.dim() != 2:
         c.fail("x", "must be [rows, channels]")
-    a = _conv_args(c, x, weight, out, bias, silu, None, state,
-                   state if state_out is None else state_out, None)
+    _, a = _conv_args(c, x, weight, out, bias, silu, None, state,
+                      state if state_out is None else state_out, None)
     c.run("zo_conv_step", a, stream=stream)
 
 
@@ -300,14 +336,14 @@ def zo_conv_backward(x, weight, dout, dx, dweight, bias=None, dbias=None, silu=T
     c = _Call("zo_conv_backward", x)
     if x.dim() != 3:
         c.fail("x", "must be [rows, seq, channels]")
-    a = _conv_args(c, x, weight, None, bias, silu, lengths, state_in, None, None)
-    dt, (R, _, D), K, S = x.dtype, x.shape, a.taps, a.sets
-    st = [_NO_TENSOR if K == 1 else c.act(n, t, (R, K - 1, D), dt, True)
+    (K, S), a = _conv_args(c, x, weight, None, bias, silu, lengths, state_in, None, None)
+    dt, (R, _, D) = x.dtype, x.shape
+    st = [_NONE3 if K == 1 else c.act(n, t, (R, K - 1, D), dt, True)
           for n, t in (("dstate_out", dstate_out), ("dstate_in", dstate_in))]
-    g = ConvGrads(c.act("dout", dout, x.shape, dt), c.act("dx", dx, x.shape, dt),
-                  c.grad("dweight", dweight, (K, D), S), c.grad("dbias", dbias, (D,), S, True),
-                  st[0], st[1])
-    need = load_library().zo_conv_backward_workspace(a)
+    g = _PACK[ConvGrads](*c.act("dout", dout, x.shape, dt), *c.act("dx", dx, x.shape, dt),
+                         *c.grad("dweight", dweight, (K, D), S),
+                         *c.grad("dbias", dbias, (D,), S, True), *st[0], *st[1])
+    need = _call("zo_conv_backward_workspace")(a)
     c.run("zo_conv_backward", a, g, stream=stream, workspace=(workspace, need))
 
 
@@ -330,21 +366,22 @@ def _scan_args(c, u, delta, A, B, C, out, skip, z, delta_bias, softplus, lengths
     G, N = B.shape[-2:]
     S = _sets((A, 2), (skip, 1), (delta_bias, 1))
     shp = (*u.shape[:-1], G, N)
-    kept = None
+    kept = 0
     if checkpoints is not None:
         c.check("checkpoints", checkpoints, torch.float32)
         if checkpoints.shape != (R, -(-T // ZO_SCAN_CHUNK), D, N) or \
                 not checkpoints.is_contiguous():
             c.fail("checkpoints", "must be contiguous of zo_scan_checkpoint_shape()")
         kept = checkpoints.data_ptr()
-    return ScanArgs(
+    return (N, S), _PACK[ScanArgs](
         R, T, D, G, N, S, c.code(u), ZO_SCAN_SOFTPLUS if softplus else 0,
-        c.act("u", u, u.shape, dt), c.act("delta", delta, u.shape, dt),
-        c.act("out", out, u.shape, dt, True), c.act("z", z, u.shape, dt, True),
-        c.act("B", B, shp, dt, inner=2), c.act("C", C, shp, dt, inner=2), c.param("A", A, (D, N), S),
-        c.param("skip", skip, (D,), S, True), c.param("delta_bias", delta_bias, (D,), S, True),
-        c.ints("lengths", lengths, R), c.states("state_in", state_in, (R, D, N)),
-        c.states("state_out", state_out, (R, D, N)), kept, c.ints("status", status, 1))
+        *c.act("u", u, u.shape, dt), *c.act("delta", delta, u.shape, dt),
+        *c.act("out", out, u.shape, dt, True), *c.act("z", z, u.shape, dt, True),
+        *c.act("B", B, shp, dt, inner=2), *c.act("C", C, shp, dt, inner=2),
+        *c.param("A", A, (D, N), S), *c.param("skip", skip, (D,), S, True),
+        *c.param("delta_bias", delta_bias, (D,), S, True), c.ints("lengths", lengths, R),
+        *c.states("state_in", state_in, (R, D, N)), *c.states("state_out", state_out, (R, D, N)),
+        kept, c.ints("status", status, 1))
 
 
 def zo_scan(u, delta, A, B, C, out, skip=None, z=None, delta_bias=None, softplus=True,
@@ -359,9 +396,9 @@ def zo_scan(u, delta, A, B, C, out, skip=None, z=None, delta_bias=None, softplus
     c = _Call("zo_scan", u)
     if u.dim() != 3:
         c.fail("u", "must be [rows, seq, channels]")
-    a = _scan_args(c, u, delta, A, B, C, out, skip, z, delta_bias, softplus, lengths, state_in,
-                   state_out, checkpoints, status)
-    need = load_library().zo_scan_workspace(a)
+    _, a = _scan_args(c, u, delta, A, B, C, out, skip, z, delta_bias, softplus, lengths, state_in,
+                      state_out, checkpoints, status)
+    need = _call("zo_scan_workspace")(a)
     c.run("zo_scan", a, stream=stream, workspace=(workspace, need))
 
 
@@ -373,8 +410,8 @@ def zo_scan_step(u, delta, A, B, C, state, out, skip=None, z=None, delta_bias=No
     c = _Call("zo_scan_step", u)
     if u.dim() != 2:
         c.fail("u", "must be [rows, channels]")
-    a = _scan_args(c, u, delta, A, B, C, out, skip, z, delta_bias, softplus, None, state,
-                   state if state_out is None else state_out, None, None)
+    _, a = _scan_args(c, u, delta, A, B, C, out, skip, z, delta_bias, softplus, None, state,
+                      state if state_out is None else state_out, None, None)
     c.run("zo_scan_step", a, stream=stream)
 
 
@@ -388,17 +425,18 @@ def zo_scan_backward(u, delta, A, B, C, dout, checkpoints, du, ddelta, dA, dB, d
     c = _Call("zo_scan_backward", u)
     if u.dim() != 3:
         c.fail("u", "must be [rows, seq, channels]")
-    a = _scan_args(c, u, delta, A, B, C, None, skip, z, delta_bias, softplus, lengths, None, None,
-                   checkpoints, None)
-    dt, (R, _, D), N, S = u.dtype, u.shape, a.states, a.sets
-    g = ScanGrads(
-        c.act("dout", dout, u.shape, dt), c.act("du", du, u.shape, dt),
-        c.act("ddelta", ddelta, u.shape, dt), c.act("dz", dz, u.shape, dt, True),
-        c.act("dB", dB, B.shape, dt, inner=2), c.act("dC", dC, B.shape, dt, inner=2),
-        c.grad("dA", dA, (D, N), S),
-        c.grad("dskip", dskip, (D,), S, True), c.grad("ddelta_bias", ddelta_bias, (D,), S, True),
-        c.states("dstate_out", dstate_out, (R, D, N)), c.states("dstate_in", dstate_in, (R, D, N)))
-    need = load_library().zo_scan_backward_workspace(a)
+    (N, S), a = _scan_args(c, u, delta, A, B, C, None, skip, z, delta_bias, softplus, lengths,
+                           None, None, checkpoints, None)
+    dt, (R, _, D) = u.dtype, u.shape
+    g = _PACK[ScanGrads](
+        *c.act("dout", dout, u.shape, dt), *c.act("du", du, u.shape, dt),
+        *c.act("ddelta", ddelta, u.shape, dt), *c.act("dz", dz, u.shape, dt, True),
+        *c.act("dB", dB, B.shape, dt, inner=2), *c.act("dC", dC, B.shape, dt, inner=2),
+        *c.grad("dA", dA, (D, N), S), *c.grad("dskip", dskip, (D,), S, True),
+        *c.grad("ddelta_bias", ddelta_bias, (D,), S, True),
+        *c.states("dstate_out", dstate_out, (R, D, N)),
+        *c.states("dstate_in", dstate_in, (R, D, N)))
+    need = _call("zo_scan_backward_workspace")(a)
     c.run("zo_scan_backward", a, g, stream=stream, workspace=(workspace, need))
 
 
@@ -410,13 +448,13 @@ def _norm_args(c, x, x_out, n_out, o, gate, w_post, scale, w_pre, eps, gate_firs
     dt = like.dtype if like is not None else x.dtype
     R, D = x.shape
     S = _sets((w_post, 1), (scale, 1), (w_pre, 1))
-    return NormArgs(
+    return S, _PACK[NormArgs](
         R, D, S, c.code(like if like is not None else x), c.code(x),
-        ZO_NORM_GATE_FIRST if gate_first else 0, eps, c.act("x", x, x.shape, x.dtype),
-        c.act("x_out", x_out, x.shape, x.dtype, True), c.act("o", o, x.shape, dt, True),
-        c.act("gate", gate, x.shape, dt, True), c.act("n_out", n_out, x.shape, dt, True),
-        c.param("w_post", w_post, (D,), S, True), c.param("scale", scale, (D,), S, True),
-        c.param("w_pre", w_pre, (D,), S, True))
+        ZO_NORM_GATE_FIRST if gate_first else 0, eps, *c.act("x", x, x.shape, x.dtype),
+        *c.act("x_out", x_out, x.shape, x.dtype, True), *c.act("o", o, x.shape, dt, True),
+        *c.act("gate", gate, x.shape, dt, True), *c.act("n_out", n_out, x.shape, dt, True),
+        *c.param("w_post", w_post, (D,), S, True), *c.param("scale", scale, (D,), S, True),
+        *c.param("w_pre", w_pre, (D,), S, True))
 
 
 def zo_block_norm(x, x_out=None, n_out=None, o=None, gate=None, w_post=None, scale=None,
@@ -427,8 +465,8 @@ def zo_block_norm(x, x_out=None, n_out=None, o=None, gate=None, w_post=None, sca
     n_out = rms(x_out) w_pre.  Without o only the norm of x.  x may be float32 while the others
     are narrower; x_out may be x."""
     c = _Call("zo_block_norm", x)
-    a = _norm_args(c, x, x_out, n_out, o, gate, w_post, scale, w_pre, eps, gate_first,
-                   o if o is not None else n_out)
+    _, a = _norm_args(c, x, x_out, n_out, o, gate, w_post, scale, w_pre, eps, gate_first,
+                      o if o is not None else n_out)
     c.run("zo_block_norm", a, stream=stream)
 
 
@@ -440,15 +478,15 @@ def zo_block_norm_backward(x_out, dn=None, dx_out=None, dx=None, do=None, dgate=
     x_out as zo_block_norm wrote it (x itself where there is no o).  Each gradient is required
     with what it belongs to; dx may be dx_out."""
     c = _Call("zo_block_norm_backward", x_out)
-    a = _norm_args(c, x_out, x_out, None, o, gate, w_post, scale, w_pre, eps, gate_first,
-                   o if o is not None else dn)
-    xt, S, D = x_out.dtype, a.sets, (a.channels,)
+    S, a = _norm_args(c, x_out, x_out, None, o, gate, w_post, scale, w_pre, eps, gate_first,
+                      o if o is not None else dn)
+    xt, D = x_out.dtype, (x_out.shape[1],)
     dt = (o if o is not None else dn if dn is not None else x_out).dtype
     shape = x_out.shape
-    g = NormGrads(
-        c.act("dn", dn, shape, dt, True), c.act("dx_out", dx_out, shape, xt, True),
-        c.act("dx", dx, shape, xt), c.act("do", do, shape, dt, True),
-        c.act("dgate", dgate, shape, dt, True), c.grad("dw_post", dw_post, D, S, True),
-        c.grad("dscale", dscale, D, S, True), c.grad("dw_pre", dw_pre, D, S, True))
-    need = load_library().zo_block_norm_backward_workspace(a)
+    g = _PACK[NormGrads](
+        *c.act("dn", dn, shape, dt, True), *c.act("dx_out", dx_out, shape, xt, True),
+        *c.act("dx", dx, shape, xt), *c.act("do", do, shape, dt, True),
+        *c.act("dgate", dgate, shape, dt, True), *c.grad("dw_post", dw_post, D, S, True),
+        *c.grad("dscale", dscale, D, S, True), *c.grad("dw_pre", dw_pre, D, S, True))
+    need = _call("zo_block_norm_backward_workspace")(a)
     c.run("zo_block_norm_backward", a, g, stream=stream, workspace=(workspace, need))

@@ -426,7 +426,7 @@ cudaError_t launch_sum_parts(const float* part, int sets, int64_t parts, int64_t
     const int ns = sets - s0 < 65535 ? sets - s0 : 65535;
     const dim3 grid((unsigned)bx, (unsigned)ns);
     const float* p = part + (int64_t)s0 * parts * n;
-    if (parts > 64)
+    if (parts > 64 && bx * ns < kBlockSMs)  // more threads a value where there are few values
       sum_parts_kernel<32><<<grid, 1024, 0, st>>>(p, parts, n, o);
     else
       sum_parts_kernel<8><<<grid, 256, 0, st>>>(p, parts, n, o);

@@ -421,15 +421,12 @@ cudaError_t run_norm_backward(const zo_norm_args& a, const zo_norm_grads& g, flo
   const int64_t blocks = (int64_t)groups / (block_of<W>() / W) * a.sets, D = a.channels;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   constexpr int kSmem = V * E > 8 ? 3 * V * E * W * (int)sizeof(float) : 0;
-  if (kSmem > 0) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_backward_kernel<T, XT, V, E, W>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = allow_shared(norm_backward_kernel<T, XT, V, E, W>, kSmem);
+  if (e != cudaSuccess) return e;
   norm_backward_kernel<T, XT, V, E, W><<<(unsigned)blocks, block_of<W>(), kSmem, st>>>(
       a, g, a.rows / a.sets, groups, params_aligned({&a.w_post, &a.scale, &a.w_pre}), ws);
   count_launch();
-  const cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const SumOut outs[3] = {{g.dw_pre, D}, {g.dw_post, D}, {g.dscale, D}};
   return launch_sum_parts(ws, a.sets, groups, 3 * D, outs, 3, st);

@@ -1158,9 +1158,7 @@ cudaError_t run_scan(const zo_scan_args& a, float* ws, cudaStream_t st) {
   constexpr int kSmem = (int)sizeof(BC<T, S * LN>);
   cudaError_t e = cudaSuccess;
   if (plan.parts > 1) {
-    if ((e = cudaFuncSetAttribute(scan_kernel<T, S, LN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  kSmem)) != cudaSuccess)
-      return e;
+    if ((e = allow_shared(scan_kernel<T, S, LN, true>, kSmem)) != cudaSuccess) return e;
     scan_kernel<T, S, LN, true><<<(unsigned)(per_row * row_blocks * (plan.parts - 1)), threads, kSmem, st>>>(
         a, d, parts, (int)rows, copy, d.N % 4 == 0);
     count_launch();
@@ -1169,9 +1167,7 @@ cudaError_t run_scan(const zo_scan_args& a, float* ws, cudaStream_t st) {
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = cudaFuncSetAttribute(scan_kernel<T, S, LN, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSmem)) != cudaSuccess)
-    return e;
+  if ((e = allow_shared(scan_kernel<T, S, LN, false>, kSmem)) != cudaSuccess) return e;
   scan_kernel<T, S, LN, false><<<(unsigned)blocks, threads, kSmem, st>>>(a, d, parts, (int)rows, copy, wide);
   count_launch();
   return cudaGetLastError();
@@ -1252,9 +1248,7 @@ cudaError_t run_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, flo
   bool vec = true;
   for (const zo_tensor* t : {&a.u, &a.delta, &a.z, &g.dout})
     vec = vec && vec_width(*t, sizeof(T), d.Dg, 4) == 4;
-  if ((e = cudaFuncSetAttribute(scan_backward_kernel<T, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(B))) != cudaSuccess)
-    return e;
+  if ((e = allow_shared(scan_backward_kernel<T, LN>, (int)sizeof(B))) != cudaSuccess) return e;
   scan_backward_kernel<T, LN><<<(unsigned)blocks, B::kThreads, sizeof(B), st>>>(a, g, d, parts, sums, vec);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -26,6 +26,14 @@ inline int vec_width(const zo_tensor& t, int elem_bytes, int64_t channels, int m
 }
 
 
+// Lets a kernel have `bytes` of dynamic shared memory.
+template <class K>
+cudaError_t allow_shared(K kernel, int bytes) {
+  return bytes <= 48 * 1024
+             ? cudaSuccess
+             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 cudaError_t launch_conv(const zo_conv_args& a, cudaStream_t st);
 int64_t conv_backward_workspace(const zo_conv_args& a);
 cudaError_t launch_conv_backward(const zo_conv_args& a, const zo_conv_grads& g, float* ws,
