@@ -163,7 +163,8 @@ class _Call:
         """A tensor of this shape: rows, steps or none, and `inner` contiguous dimensions."""
         if t is None and optional:
             return _NONE3
-        self.check(name, t, dtype)
+        if t is None or t.dtype is not dtype or t.get_device() != self.index:
+            self.check(name, t, dtype)
         if t.shape != shape:
             self.fail(name, f"must have shape {tuple(shape)}, got {tuple(t.shape)}")
         st = t.stride()
@@ -177,7 +178,8 @@ class _Call:
         """Parameters [inner] or [sets, inner]."""
         if t is None and optional:
             return _NONE2
-        self.check(name, t, torch.float32)
+        if t is None or t.dtype is not torch.float32 or t.get_device() != self.index:
+            self.check(name, t, torch.float32)
         n, shape = len(inner), t.shape
         if shape[-n:] != inner or len(shape) - n not in (0, 1):
             self.fail(name, f"must have shape {tuple(inner)} or [sets, ...], got {tuple(shape)}")
@@ -203,7 +205,8 @@ class _Call:
         """Parameter gradients: one for each set."""
         if t is None and optional:
             return _NONE2
-        self.check(name, t, torch.float32)
+        if t is None or t.dtype is not torch.float32 or t.get_device() != self.index:
+            self.check(name, t, torch.float32)
         n = len(inner)
         if not (t.shape == (sets, *inner) or (sets == 1 and t.shape == inner)):
             self.fail(name, f"must have shape {(sets, *inner)}, got {tuple(t.shape)}")
@@ -214,7 +217,8 @@ class _Call:
         """Recurrent states [rows, channels, states]."""
         if t is None and optional:
             return _NONE2
-        self.check(name, t, torch.float32)
+        if t is None or t.dtype is not torch.float32 or t.get_device() != self.index:
+            self.check(name, t, torch.float32)
         if t.shape != shape:
             self.fail(name, f"must have shape {tuple(shape)}, got {tuple(t.shape)}")
         return t.data_ptr(), self.contiguous(name, t, 2)[0]

@@ -470,7 +470,8 @@ __global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims
 }
 
 // One token.  A thread holds four states of a channel and walks RG rows of a
-// set, so that A is read once for them.  Bound: the states, read and written.
+// set, so that A is read once for them; all its loads are issued before the first result is
+// waited for.  Bound: the states, read and written.  WIDE: states, B and C four at a time.
 template <class T, int LN, int RG, bool WIDE>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, ScanDims d, int64_t groups) {
   const int64_t nb = ((int64_t)d.D * LN + kThreads - 1) / kThreads;  // blocks of a row
@@ -480,35 +481,61 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, Sca
   const int64_t c = on ? i / LN : 0;
   const int64_t first = blockIdx.x / nb * RG, set = first / groups;
   const int64_t r0 = set * d.rows_per_set + first % groups;
-  const int g = (int)(c / d.Dg);
-  float A[4];
-  load_states4<WIDE>(a.A.ptr + set * a.A.stride + c * d.N, n0, d.N, A);
-  const float skip = a.skip.ptr ? a.skip.ptr[set * a.skip.stride + c] : 0.f;
-  const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[set * a.delta_bias.stride + c] : 0.f;
+  const int have = (int)(d.rows_per_set - first % groups);  // rows of the set from r0 on
+  const int64_t g = c / d.Dg;
+  auto four = [&](auto* p, int n, bool there) {  // p[n ..], zeros from N on
+    using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    if constexpr (WIDE) {
+      return load_if<E, 4>(p + n, there && n < d.N);
+    } else {
+      Vec<E, 4> x;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
+      for (int j = 0; j < 4; ++j) x.v[j] = load_if<E, 1>(p + n + j, there && n + j < d.N).v[0];
+      return x;
+    }
+  };
+  Vec<float, 4> h[RG];
+  Vec<T, 4> B[RG], C[RG];
+  T u[RG], dl[RG], z[RG];
 #pragma unroll
   for (int k = 0; k < RG; ++k) {
     const int64_t row = r0 + k;
-    if (RG > 1 && first % groups + k >= d.rows_per_set) break;
-    float h[4] = {0.f, 0.f, 0.f, 0.f}, B[4], C[4], y = 0.f;
-    if (on) load_states4<WIDE>(a.state_in.ptr + row * a.state_in.stride + c * d.N, n0, d.N, h);
-    load_states(static_cast<const T*>(a.B.ptr) + row * a.B.row + (int64_t)g * d.N, n0, d.N, B);
-    load_states(static_cast<const T*>(a.C.ptr) + row * a.C.row + (int64_t)g * d.N, n0, d.N, C);
-    const float u = to_f(static_cast<const T*>(a.u.ptr)[row * a.u.row + c]);
-    float dt = to_f(static_cast<const T*>(a.delta.ptr)[row * a.delta.row + c]) + bias;
-    if (a.flags & ZO_SCAN_SOFTPLUS) dt = softplus_f(dt);
+    const bool there = on && k < have;
+    h[k] = four(static_cast<const float*>(a.state_in.ptr) + row * a.state_in.stride + c * d.N, n0, there);
+    B[k] = four(static_cast<const T*>(a.B.ptr) + row * a.B.row + g * d.N, n0, there);
+    C[k] = four(static_cast<const T*>(a.C.ptr) + row * a.C.row + g * d.N, n0, there);
+    u[k] = load_if<T, 1>(static_cast<const T*>(a.u.ptr) + row * a.u.row + c, there).v[0];
+    dl[k] = load_if<T, 1>(static_cast<const T*>(a.delta.ptr) + row * a.delta.row + c, there).v[0];
+    z[k] = load_if<T, 1>(static_cast<const T*>(a.z.ptr) + row * a.z.row + c, there && a.z.ptr).v[0];
+  }
+  float A[4];
+  load_states(a.A.ptr + set * a.A.stride + c * d.N, n0, d.N, A);
+  const float2 A2[2] = {make_float2(A[0] * kLog2e, A[1] * kLog2e), make_float2(A[2] * kLog2e, A[3] * kLog2e)};
+  const float skip = a.skip.ptr ? a.skip.ptr[set * a.skip.stride + c] : 0.f;
+  const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[set * a.delta_bias.stride + c] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = fmaf(exp2_1(dt * A[i]), h[i], dt * u * B[i]);
-      y = fmaf(C[i], h[i], y);
+  for (int k = 0; k < RG; ++k) {
+    if (k >= have) break;
+    const int64_t row = r0 + k;
+    const float uk = to_f(u[k]);
+    float dt = to_f(dl[k]) + bias;
+    if (a.flags & ZO_SCAN_SOFTPLUS) dt = softplus_f(dt);
+    const float2 x = two(dt * uk);
+    float2 y = two(0.f);
+    float f[4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float2 v = __ffma2_rn(exp2_2(__fmul2_rn(two(dt), A2[p])), make_float2(h[k].v[2 * p], h[k].v[2 * p + 1]),
+                                  __fmul2_rn(x, make_float2(to_f(B[k].v[2 * p]), to_f(B[k].v[2 * p + 1]))));
+      y = __ffma2_rn(make_float2(to_f(C[k].v[2 * p]), to_f(C[k].v[2 * p + 1])), v, y);
+      f[2 * p] = v.x, f[2 * p + 1] = v.y;
     }
     if (on && a.state_out.ptr)
-      store_states4<WIDE>(a.state_out.ptr + row * a.state_out.stride + c * d.N, n0, d.N, h);
-    y = fmaf(skip, u, sum_lanes<LN>(y));
+      store_states4<WIDE>(a.state_out.ptr + row * a.state_out.stride + c * d.N, n0, d.N, f);
+    float out = fmaf(skip, uk, sum_lanes<LN>(y.x + y.y));
     if (on && q == 0) {
-      if (a.z.ptr) y *= silu_2(two(to_f(static_cast<const T*>(a.z.ptr)[row * a.z.row + c]))).x;
-      static_cast<T*>(a.out.ptr)[row * a.out.row + c] = from_f<T>(y);
+      if (a.z.ptr) out *= silu_2(two(to_f(z[k]))).x;
+      static_cast<T*>(a.out.ptr)[row * a.out.row + c] = from_f<T>(out);
     }
   }
 }
@@ -902,6 +929,16 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
     }
     float2 h0[4][2];
     load_lane(a.checkpoints + ((row * d.chunks + t0 / kChunk) * d.D + c0) * d.N, h0);
+    if (t0 - kChunk >= tb) {  // the chunk before: its inputs come nearer meanwhile
+      constexpr int kLine = 128 / (int)sizeof(T), kLines = (S::kChannels + kLine - 1) / kLine;
+      for (int i = tid; i < 4 * kChunk * kLines; i += S::kThreads) {
+        const int c = i % kLines * kLine, which = i / kLines % 4;
+        const int64_t t = t0 - kChunk + i / (4 * kLines);
+        const T* p = which == 0 ? bu + t * a.u.step : which == 1 ? bd + t * a.delta.step
+                     : which == 2 ? bo + t * g.dout.step : bz + t * a.z.step;
+        if (c < left && (which < 3 || gate)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
+      }
+    }
     __syncthreads();
 
     auto load4 = [&](const float2* p, float2 (&f)[4]) {
@@ -1180,8 +1217,9 @@ cudaError_t run_scan_step(const zo_scan_args& a, cudaStream_t st) {
   const int64_t blocks = ceil_div((int64_t)d.D * LN, kThreads) * (groups / RG) * a.sets;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   bool wide = d.N % 4 == 0;
-  for (const zo_f32* p : {&a.A, &a.state_in, &a.state_out})
+  for (const zo_f32* p : {&a.state_in, &a.state_out})
     wide = wide && p->stride % 4 == 0 && reinterpret_cast<uintptr_t>(p->ptr) % 16 == 0;
+  for (const zo_tensor* t : {&a.B, &a.C}) wide = wide && vec_width(*t, sizeof(T), 4, 4) == 4;
   if (wide)
     scan_step_kernel<T, LN, RG, true><<<(unsigned)blocks, kThreads, 0, st>>>(a, d, groups);
   else
