@@ -30,6 +30,8 @@
  *     between calls: calls on different streams do not disturb one another as
  *     long as each has its own workspace and outputs, and a call can be captured
  *     into a CUDA graph.
+ *   - There is at least one row and one step; steps and channels are at most
+ *     2^30.
  *   - All pointers are device pointers owned by the caller, aligned to their
  *     element type.  Strides count elements and may be any value that keeps
  *     the elements of an output apart; the innermost dimension (channels, or
@@ -134,7 +136,8 @@ typedef struct zo_scan_args {
   zo_tensor u, delta, out;    /* [rows][seq][channels]                            */
   zo_tensor z;                /* the gate; optional                               */
   zo_tensor B, C;             /* [rows][seq][groups * N]                          */
-  zo_f32 A;                   /* [sets][channels][N]                              */
+  zo_f32 A;                   /* [sets][channels][N]; beyond 2.3e38 (the largest  */
+                              /* fp32 over log2(e)) it counts as that             */
   zo_f32 skip, delta_bias;    /* [sets][channels]; optional                       */
   const int32_t* lengths;     /* [rows], optional: steps of each row, 0..seq      */
   zo_f32 state_in;            /* [rows][channels][N]; optional (zeros)            */

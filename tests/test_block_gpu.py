@@ -104,6 +104,8 @@ CONV = [  # R, T, D, K, S, dtype, ragged, state, pad, act
     (1, 700, 520, 4, 1, "bf16", None, False, False, True),
     (2, 31, 33, 6, 2, "f32", True, True, True, True),
     (3, 5, 8, 7, 1, "f16", True, True, False, False),
+    (2, 3000, 24, 4, 1, "bf16", True, True, False, True),
+    (3, 40, 30, 4, 3, "bf16", True, True, False, True),
 ]
 
 
@@ -183,6 +185,9 @@ SCAN = [  # R, T, D, G, N, S, dtype, ragged, state, gate, softplus, pad
     (1, 65, 8, 8, 33, 1, "f16", None, False, True, True, False),
     (5, 2, 96, 1, 16, 5, "bf16", True, True, True, True, True),
     (1, 2500, 16, 1, 16, 1, "f32", None, True, True, True, False),
+    (230, 1100, 8, 1, 16, 2, "f32", True, False, True, True, False),
+    (6000, 5, 8, 1, 16, 3, "bf16", True, True, True, True, False),
+    (2600, 40, 40, 1, 8, 1, "f16", True, False, True, True, False),
 ]
 
 
@@ -289,6 +294,38 @@ def test_scan_steps_equal_the_prompt(D, G, N, dtype, gate):
     near(y, want, size, ops, "steps")
     near(now, last, slast, ops, "state")
     near(so, last, slast, ops, "prompt's state")
+
+
+@pytest.mark.parametrize("A", [-3.4e38, -1e30, -1e-30, 0.0, 0.3])
+def test_scan_extreme_decays(A):
+    """Decays of 0 and 1 and above, steps of length 0 between them, and their gradients."""
+    R, T, D, N = 2, 40, 8, 4
+    i = Inputs(7, False)
+    u, B, C, dout = i.normal(R, T, D), i.normal(R, T, 1, N), i.normal(R, T, 1, N), i.normal(R, T, D)
+    dl = i.normal(R, T, D).abs() * (torch.rand(R, T, D, generator=i.g, device="cuda") < 0.7)
+    a, st = torch.full((1, D, N), A, device="cuda"), i.normal(R, D, N)
+    out, so = torch.empty_like(u), torch.empty_like(st)
+    kept = torch.empty(zo.zo_scan_checkpoint_shape(u.shape, N), device="cuda")
+    zo.zo_scan(u, dl, a, B, C, out, softplus=False, state_in=st, state_out=so, checkpoints=kept)
+    args = (u, dl, a, B, C, None, None, None, False, None, st)
+    (want, last, _, _), (size, slast, _, _) = ref.scan(*args), ref.scan(*args, size=True)
+    # |d A| matters only where the decay is not 0: up to 104, from where fp32 has none
+    ops = T * (8 + 8 * min(104.0, float(dl.max()) * abs(A))) + 64
+    near(out, want, size, ops, "out")
+    near(so, last, slast, ops, "state")
+    g = {k: torch.empty_like(t) for k, t in {"du": u, "ddelta": dl, "dA": a, "dB": B, "dC": C}.items()}
+    zo.zo_scan_backward(u, dl, a, B, C, dout, kept, g["du"], g["ddelta"], g["dA"], g["dB"], g["dC"], softplus=False)
+    # rates count up to the largest fp32 over log2(e) (include/zo_block.h)
+    args = (u, dl, a.double().clamp(min=-torch.finfo(torch.float32).max / 1.4426950408889634), B, C,
+            dout, None, None, None, False, None, st)
+    want, size = ref.scan_backward(*args), ref.scan_backward(*args, size=True)
+    for k in g:
+        # at steps of length 0, ddelta has terms g A h, which are summed as g (A log2(e)) h: where
+        # those add up to more than the largest fp32, 3.4e38, each or a partial sum can be
+        # infinite though the sum is not, and fp32 has no answer
+        fits = size[k] * 1.4426950408889634 < torch.finfo(torch.float32).max
+        near(g[k][fits], want[k][fits], size[k][fits], 2 * ops + T * R, k)
+        assert fits.all() or (k == "ddelta" and A < -1e37)
 
 
 def test_scan_gradient_against_differences():

@@ -50,12 +50,12 @@ def norm_args(**kw):
     return a
 
 
-BAD_SIZES = [dict(rows=0), dict(rows=-1), dict(channels=0), dict(sets=0), dict(sets=3), dict(dtype=7), dict(flags=8)]
+BAD_SIZES = [dict(rows=0), dict(rows=-1), dict(channels=0), dict(channels=2 ** 30 + 2), dict(sets=0), dict(sets=3), dict(dtype=7), dict(flags=8)]
 T0, F0 = block._Tensor(), block._F32()
 
 
 @pytest.mark.parametrize("kw", BAD_SIZES + [
-    dict(seq=0), dict(taps=0), dict(x=T0), dict(out=T0), dict(weight=F0), dict(x=block._Tensor(P + 2, 64, 8)),
+    dict(seq=0), dict(seq=2 ** 30 + 1), dict(taps=0), dict(x=T0), dict(out=T0), dict(weight=F0), dict(x=block._Tensor(P + 2, 64, 8)),
     dict(out=block._Tensor(P, 64, 8)), dict(out=block._Tensor(2 * P, 64, 7)), dict(out=block._Tensor(2 * P, 16, 8)),
     dict(lengths=P + 1), dict(state_in=block._Tensor(P + 1, 24, 8)), dict(state_out=block._Tensor(3 * P, 16, 8)),
     dict(state_in=block._Tensor(3 * P, 24, 8), state_out=block._Tensor(3 * P, 32, 8))])
@@ -84,7 +84,7 @@ def test_conv_refuses_more():
 
 
 @pytest.mark.parametrize("kw", BAD_SIZES + [
-    dict(seq=0), dict(groups=0), dict(groups=3), dict(states=0), dict(u=T0), dict(delta=T0), dict(B=T0), dict(C=T0),
+    dict(seq=0), dict(seq=2 ** 30 + 1), dict(groups=0), dict(groups=3), dict(states=0), dict(u=T0), dict(delta=T0), dict(B=T0), dict(C=T0),
     dict(A=F0), dict(out=T0), dict(out=block._Tensor(P, 64, 8)), dict(out=block._Tensor(2 * P, 0, 8)),
     dict(checkpoints=P + 4), dict(state_out=block._F32(3 * P, 64)),
     dict(state_in=block._F32(3 * P, 128), state_out=block._F32(3 * P, 256))])

@@ -1,9 +1,12 @@
 // Selective scan: per row, channel and state h_t = exp(d_t A) h_{t-1} + d_t u_t B_t,
 // y_t = sum_n C_t h_t + skip u_t, out_t = y_t silu(z_t), d_t = softplus(delta_t + bias);
-// its gradients; and its single-token form.
+// its gradients; and its single-token form.  States, carries and sums are fp32.
 //
-// A channel's states lie on LN lanes, four each; a warp walks 32 / LN channels
-// through time.
+// exp(d A) is 2^(d A log2(e)) by the special function unit (2^-22 relative).  It is not the
+// tensor cores' work: every channel and state has its own decay at every step, so no step is
+// a matrix product.  Times below are at 16 states and bf16.
+#include <float.h>
+
 #include <initializer_list>
 #include <type_traits>
 
@@ -34,10 +37,12 @@ __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t ro
   return n < 0 ? 0 : T;
 }
 
-// 2^x, more exactly for |x| < 1/16: the special function unit's results there are too small by
-// 1e-7 of themselves on average (they are cut off, measured), which over the 1 / |x| steps
-// that such a decay lasts adds up to 1e-6 of a state.  A polynomial of degree 3, 1 at 0, with the least largest relative error up to 1/16
-// (2.7e-8; its coefficients are the solution of that linear programme).
+// 2^x, more exactly for |x| < 1/16.  The special function unit's results there are too small by
+// 6e-8 of themselves on average (measured: they are cut off rather than rounded), which over the
+// 1 / |x| steps that such a decay lasts adds up to 1e-6 of a state; so there a polynomial of
+// degree 3 that is 1 at 0 and has the least largest relative error up to 1/16 (2.7e-8; its
+// coefficients are the solution of that linear programme).  The backward pass uses it for the
+// carries, which halves the error of dA.
 __device__ __forceinline__ float2 exp2_slow_2(float2 x) {
   const float2 e = exp2_2(x);
   float2 p = __ffma2_rn(x, two(0.0554962232708931f), two(0.2402576357126236f));
@@ -45,6 +50,14 @@ __device__ __forceinline__ float2 exp2_slow_2(float2 x) {
   p = __ffma2_rn(x, p, two(1.f));
   return make_float2(fabsf(x.x) < 0.0625f ? p.x : e.x, fabsf(x.y) < 0.0625f ? p.y : e.y);
 }
+
+// A log2(e), kept finite: the lowest fp32 as a decay rate gives decays of 0 and, at steps of
+// length 0, of 1.
+__device__ __forceinline__ float rate(float A) {
+  const float v = A * kLog2e;
+  return fabsf(v) > FLT_MAX ? copysignf(FLT_MAX, v) : v;
+}
+__device__ __forceinline__ float2 rate_2(float2 A) { return make_float2(rate(A.x), rate(A.y)); }
 
 // max(x, 0), NaN for NaN
 __device__ __forceinline__ float relu_nan(float x) {
@@ -84,29 +97,6 @@ __device__ __forceinline__ float sum_lanes(float v) {
 #pragma unroll
   for (int m = LN / 2; m > 0; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
-}
-
-// Where a thread works: its row, group, channel and first state.
-struct Place {
-  int64_t row, set;
-  int g, c, n0, tile;
-  bool on;  // its channel exists (its lanes take part in shuffles either way)
-};
-
-template <int LN>
-__device__ __forceinline__ Place place(const ScanDims& d, int64_t block) {
-  Place p;
-  constexpr int CT = kThreads / LN;
-  p.tile = (int)(block % d.tiles);
-  block /= d.tiles;
-  p.g = (int)(block % d.G);
-  p.row = block / d.G;
-  p.set = p.row / d.rows_per_set;
-  const int k = p.tile * CT + (int)threadIdx.x / LN;
-  p.on = k < d.Dg;
-  p.c = p.g * d.Dg + (p.on ? k : 0);
-  p.n0 = ((int)threadIdx.x % LN) * 4;
-  return p;
 }
 
 template <class T>
@@ -264,7 +254,7 @@ __global__ void __launch_bounds__(128, 4)
   float2 A2[H];
   load_pairs<S>(a.A.ptr + set * a.A.stride + c * d.N, n0, d.N, false, A2);
 #pragma unroll
-  for (int i = 0; i < H; ++i) A2[i] = __fmul2_rn(A2[i], two(kLog2e));
+  for (int i = 0; i < H; ++i) A2[i] = rate_2(A2[i]);
   const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[set * a.delta_bias.stride + c] : 0.f;
   const float skip = !LOCAL && a.skip.ptr ? a.skip.ptr[set * a.skip.stride + c] : 0.f;
   const bool softplus = a.flags & ZO_SCAN_SOFTPLUS, gate = !LOCAL && a.z.ptr;
@@ -448,7 +438,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, DN = (int64_t)d.D * d.N;
   if (i >= a.rows * DN) return;
   const int64_t row = i / DN, cn = i % DN, c = cn / d.N, set = row / d.rows_per_set;
-  const float A2 = a.A.ptr[set * a.A.stride + cn] * kLog2e;
+  const float A2 = rate(a.A.ptr[set * a.A.stride + cn]);
   float h = a.state_in.ptr ? a.state_in.ptr[row * a.state_in.stride + cn] : 0.f;
   float* state = parts.state + row * parts.n * DN + cn;
   const float* sum = parts.sum + row * parts.n * d.D + c;
@@ -510,7 +500,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, Sca
   }
   float A[4];
   load_states(a.A.ptr + set * a.A.stride + c * d.N, n0, d.N, A);
-  const float2 A2[2] = {make_float2(A[0] * kLog2e, A[1] * kLog2e), make_float2(A[2] * kLog2e, A[3] * kLog2e)};
+  const float2 A2[2] = {make_float2(rate(A[0]), rate(A[1])), make_float2(rate(A[2]), rate(A[3]))};
   const float skip = a.skip.ptr ? a.skip.ptr[set * a.skip.stride + c] : 0.f;
   const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[set * a.delta_bias.stride + c] : 0.f;
 #pragma unroll
@@ -602,7 +592,7 @@ __global__ void __launch_bounds__(128, 4)
   load_pairs<S>(a.A.ptr + set * a.A.stride + c * d.N, n0, d.N, false, A2);
 #pragma unroll
   for (int i = 0; i < H; ++i) {
-    A2[i] = __fmul2_rn(A2[i], two(kLog2e));
+    A2[i] = rate_2(A2[i]);
     v[i] = two(0.f);
   }
   const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[set * a.delta_bias.stride + c] : 0.f;
@@ -691,7 +681,7 @@ __global__ void __launch_bounds__(256) carry_join_kernel(zo_scan_args a, zo_scan
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, DN = (int64_t)d.D * d.N;
   if (i >= a.rows * DN) return;
   const int64_t row = i / DN, cn = i % DN, c = cn / d.N, set = row / d.rows_per_set;
-  const float A2 = a.A.ptr[set * a.A.stride + cn] * kLog2e;
+  const float A2 = rate(a.A.ptr[set * a.A.stride + cn]);
   float v = g.dstate_out.ptr ? g.dstate_out.ptr[row * g.dstate_out.stride + cn] : 0.f;
   float* state = parts.state + row * parts.n * DN + cn;
   const float* sum = parts.sum + row * parts.n * d.D + c;
@@ -805,7 +795,7 @@ __global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / 
   for (int n = 0; n < 4; ++n)
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      A2[n][p] = __fmul2_rn(A2[n][p], two(kLog2e));
+      A2[n][p] = rate_2(A2[n][p]);
       dA[n][p] = two(0.f);
     }
 

@@ -43,10 +43,11 @@ bool maybe(const zo_tensor& t, int bytes) { return aligned(t.ptr, bytes); }
 bool here(const zo_f32& t) { return t.ptr && aligned(t.ptr, 4); }
 bool maybe(const zo_f32& t) { return aligned(t.ptr, 4); }
 
-// rows and sets that divide them; sizes whose products stay below 2^62
+// Sets divide the rows; steps and channels leave 32-bit arithmetic room for a tile more.
 bool shape_ok(int32_t rows, int32_t seq, int32_t channels, int32_t sets, int32_t dtype) {
-  return rows >= 1 && seq >= 1 && channels >= 1 && sets >= 1 && rows % sets == 0 &&
-         dtype_ok(dtype) && (int64_t)rows * seq < (1ll << 40);
+  constexpr int32_t kMost = 1 << 30;
+  return rows >= 1 && seq >= 1 && seq <= kMost && channels >= 1 && channels <= kMost && sets >= 1 &&
+         rows % sets == 0 && dtype_ok(dtype);
 }
 
 // An output with several rows (steps) must not lay one over another.
