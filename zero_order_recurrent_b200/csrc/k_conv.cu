@@ -18,11 +18,14 @@ namespace zo {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int V = 4;  // channels a thread
+
+// Blocks of an SM that the registers allow.
+constexpr int held_forward(int taps) { return taps <= 4 ? 7 : taps <= 6 ? 5 : 4; }
+constexpr int held_backward(int taps) { return taps <= 4 ? 4 : taps <= 5 ? 3 : 2; }
 
 struct ConvDims {
   int T, D, rows_per_set, run, runs, ctiles;
-  bool params;  // the parameters' rows start on 16 bytes
+  bool params;  // the parameters' rows can be accessed by vectors
 };
 
 __device__ __forceinline__ int row_length(const int32_t* lengths, int64_t row, int T,
@@ -34,10 +37,10 @@ __device__ __forceinline__ int row_length(const int32_t* lengths, int64_t row, i
   return n < 0 ? 0 : T;
 }
 
-// Four channels from p, of which `have` exist (VEC: always all, on a vector's boundary); zeros
+// V channels from p, of which `have` exist (VEC: always all, on a vector's boundary); zeros
 // where `on` is false.
-template <class T, bool VEC>
-__device__ __forceinline__ Vec<T, V> load4(const T* p, int have, bool on) {
+template <class T, int V, bool VEC>
+__device__ __forceinline__ Vec<T, V> load_channels(const T* p, int have, bool on) {
   if constexpr (VEC) {
     return load_if<T, V>(p, on);
   } else {
@@ -48,44 +51,50 @@ __device__ __forceinline__ Vec<T, V> load4(const T* p, int have, bool on) {
   }
 }
 
-template <class T, bool VEC>
-__device__ __forceinline__ void store4(T* p, int have, const float2 (&f)[2]) {
-  Vec<T, V> x;
-  x.v[0] = from_f<T>(f[0].x), x.v[1] = from_f<T>(f[0].y);
-  x.v[2] = from_f<T>(f[1].x), x.v[3] = from_f<T>(f[1].y);
+template <class T, bool VEC, int P>
+__device__ __forceinline__ void store_channels(T* p, int have, const float2 (&f)[P]) {
+  Vec<T, 2 * P> x;
+#pragma unroll
+  for (int i = 0; i < P; ++i) x.v[2 * i] = from_f<T>(f[i].x), x.v[2 * i + 1] = from_f<T>(f[i].y);
   if constexpr (VEC) {
-    *reinterpret_cast<Vec<T, V>*>(p) = x;
+    *reinterpret_cast<Vec<T, 2 * P>*>(p) = x;
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < 2 * P; ++i)
       if (i < have) p[i] = x.v[i];
   }
 }
 
-template <class T>
-__device__ __forceinline__ void pairs_of(const Vec<T, V>& x, float2 (&f)[2]) {
-  f[0] = make_float2(to_f(x.v[0]), to_f(x.v[1]));
-  f[1] = make_float2(to_f(x.v[2]), to_f(x.v[3]));
+template <class T, int P>
+__device__ __forceinline__ void pairs_of(const Vec<T, 2 * P>& x, float2 (&f)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) f[i] = make_float2(to_f(x.v[2 * i]), to_f(x.v[2 * i + 1]));
 }
 
-__device__ __forceinline__ void load_params(const float* p, int have, bool vec, float2 (&f)[2]) {
-  Vec<float, V> x;
+template <int P>
+__device__ __forceinline__ void load_params(const float* p, int have, bool vec, float2 (&f)[P]) {
+  Vec<float, 2 * P> x;
   if (vec) {
-    x = *reinterpret_cast<const Vec<float, V>*>(p);
+    x = *reinterpret_cast<const Vec<float, 2 * P>*>(p);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) x.v[i] = i < have ? p[i] : 0.f;
+    for (int i = 0; i < 2 * P; ++i) x.v[i] = i < have ? p[i] : 0.f;
   }
   pairs_of(x, f);
 }
 
-__device__ __forceinline__ void zero(float2 (&f)[2]) { f[0] = f[1] = two(0.f); }
+template <int P>
+__device__ __forceinline__ void zero(float2 (&f)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) f[i] = two(0.f);
+}
 
 // Where a thread works.
 struct Place {
   int run, c, have;
   int64_t row, set;
 };
+template <int V>
 __device__ __forceinline__ Place place(const ConvDims& d) {
   Place p;
   const unsigned rest = blockIdx.x / (unsigned)d.ctiles;
@@ -98,7 +107,7 @@ __device__ __forceinline__ Place place(const ConvDims& d) {
 }
 
 // One row's inputs: x, before it the carried window (or 0), after its length 0.
-template <class T, int K, bool VEC>
+template <class T, int K, int V, bool VEC>
 struct Inputs {
   const T *x, *s;
   int64_t x_step, s_step;
@@ -113,20 +122,21 @@ struct Inputs {
   }
   __device__ __forceinline__ Vec<T, V> at(int t) const {  // any step
     const T* p = t >= 0 ? x + t * x_step : s + (t + K - 1) * s_step;
-    return load4<T, VEC>(p, have, t >= 0 ? t < len : s != nullptr);
+    return load_channels<T, V, VEC>(p, have, t >= 0 ? t < len : s != nullptr);
   }
   __device__ __forceinline__ Vec<T, V> from_x(int t) const {  // t >= 0
-    return load4<T, VEC>(x + t * x_step, have, t < len);
+    return load_channels<T, V, VEC>(x + t * x_step, have, t < len);
   }
 };
 
-template <class T, int K, int U, bool VEC>
-__global__ void __launch_bounds__(kThreads) conv_kernel(zo_conv_args a, ConvDims d) {
-  const Place p = place(d);
+template <class T, int K, int V, int U, bool VEC>
+__global__ void __launch_bounds__(kThreads, held_forward(K)) conv_kernel(zo_conv_args a, ConvDims d) {
+  constexpr int P = V / 2;
+  const Place p = place<V>(d);
   if (p.have <= 0) return;
   const int len = row_length(a.lengths, p.row, d.T, a.status, p.run == 0 && p.c == 0);
-  const Inputs<T, K, VEC> in(a, p, len);
-  float2 w[K][2], b[2];
+  const Inputs<T, K, V, VEC> in(a, p, len);
+  float2 w[K][P], b[P];
 #pragma unroll
   for (int k = 0; k < K; ++k)
     load_params(a.weight.ptr + p.set * a.weight.stride + (int64_t)k * d.D + p.c, p.have, d.params, w[k]);
@@ -136,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(zo_conv_args a, ConvDims
   Vec<T, V> next[U];
 #pragma unroll
   for (int j = 0; j < U; ++j) next[j] = in.from_x(t0 + j);
-  float2 win[K - 1 + U][2];
+  float2 win[K - 1 + U][P];
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) pairs_of(in.at(t0 - (K - 1) + j), win[j]);
   const bool silu = a.flags & ZO_CONV_SILU;
@@ -150,22 +160,22 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(zo_conv_args a, ConvDims
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (t + j >= t1) break;
-      float2 y[2];
+      float2 y[P];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < P; ++i) {
         y[i] = b[i];
 #pragma unroll
         for (int k = 0; k < K; ++k) y[i] = __ffma2_rn(w[k][i], win[j + k][i], y[i]);
         if (silu) y[i] = silu_2(y[i]);
         if (t + j >= len) y[i] = two(0.f);
       }
-      store4<T, VEC>(out, p.have, y);
+      store_channels<T, VEC>(out, p.have, y);
       out += a.out.step;
     }
 #pragma unroll
     for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) win[j][i] = win[U + j][i];
+      for (int i = 0; i < P; ++i) win[j][i] = win[U + j][i];
   }
   // The window after the row's last step.  Only the first run reads state_in, so
   // the same thread may write it in place: all loads come before the stores.
@@ -174,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(zo_conv_args a, ConvDims
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) pairs_of(in.at(len - (K - 1) + j), win[j]);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) store4<T, VEC>(so + j * a.state_out.step, p.have, win[j]);
+    for (int j = 0; j < K - 1; ++j) store_channels<T, VEC>(so + j * a.state_out.step, p.have, win[j]);
   }
 }
 
@@ -182,21 +192,22 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(zo_conv_args a, ConvDims
 // gradient sends to p);  dw[k] += d_t x_{t-K+1+k};  db += d_t.
 // The run of steps [t0, t1) owns d_t for the sums, and gives dx_p for p in [t0, t1);
 // the first run also for p < 0, which is the carried window's gradient.
-template <class T, int K, int U, bool VEC>
-__global__ void __launch_bounds__(kThreads, K <= 4 ? 4 : K <= 5 ? 3 : 2)
+template <class T, int K, int V, int U, bool VEC>
+__global__ void __launch_bounds__(kThreads, held_backward(K))
     conv_backward_kernel(zo_conv_args a, zo_conv_grads g, ConvDims d, float* part) {
-  const Place p = place(d);
+  constexpr int P = V / 2;
+  const Place p = place<V>(d);
   if (p.have <= 0) return;
   const int len = row_length(a.lengths, p.row, d.T, a.status, p.run == 0 && p.c == 0);
-  const Inputs<T, K, VEC> in(a, p, len);
+  const Inputs<T, K, V, VEC> in(a, p, len);
   const T* dout = static_cast<const T*>(g.dout.ptr) + p.row * g.dout.row + p.c;
   const T* dso = K > 1 && g.dstate_out.ptr
                      ? static_cast<const T*>(g.dstate_out.ptr) + p.row * g.dstate_out.row + p.c
                      : nullptr;
   T* dx = static_cast<T*>(g.dx.ptr) + p.row * g.dx.row + p.c;
   T* dsi = K > 1 && g.dstate_in.ptr ? static_cast<T*>(g.dstate_in.ptr) + p.row * g.dstate_in.row + p.c : nullptr;
-  auto dout_at = [&](int t) { return load4<T, VEC>(dout + t * g.dout.step, p.have, t < len); };
-  float2 w[K][2], b[2], dw[K][2], db[2];
+  auto dout_at = [&](int t) { return load_channels<T, V, VEC>(dout + t * g.dout.step, p.have, t < len); };
+  float2 w[K][P], b[P], dw[K][P], db[P];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     load_params(a.weight.ptr + p.set * a.weight.stride + (int64_t)k * d.D + p.c, p.have, d.params, w[k]);
@@ -211,14 +222,14 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 4 : K <= 5 ? 3 : 2)
   Vec<T, V> nx[U], ny[U];
 #pragma unroll
   for (int j = 0; j < U; ++j) nx[j] = in.from_x(t0 + j), ny[j] = dout_at(t0 + j);
-  float2 xw[K - 1 + U][2], dd[K - 1 + U][2];  // x_{t-K+1..}, d_{t-K+1..}
+  float2 xw[K - 1 + U][P], dd[K - 1 + U][P];  // x_{t-K+1..}, d_{t-K+1..}
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
     pairs_of(in.at(t0 - (K - 1) + j), xw[j]);
     zero(dd[j]);
   }
   for (int t = t0; t < last; t += U) {
-    float2 dy[U][2];
+    float2 dy[U][P];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       pairs_of(nx[j], xw[K - 1 + j]);
@@ -230,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 4 : K <= 5 ? 3 : 2)
 #pragma unroll
     for (int j = 0; j < U; ++j) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < P; ++i) {
         float2 v = dy[j][i];  // 0 behind the row's end
         if (silu) {
           float2 pre = b[i], s, slope;
@@ -248,28 +259,28 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 4 : K <= 5 ? 3 : 2)
       }
       const int q = t + j - (K - 1);  // whose gradient is now complete
       if (q >= p0 && q < t1) {
-        float2 o[2];
+        float2 o[P];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < P; ++i) {
           o[i] = two(0.f);
 #pragma unroll
           for (int k = 0; k < K; ++k) o[i] = __ffma2_rn(w[k][i], dd[j + K - 1 - k][i], o[i]);
         }
         const int r = t + j - len;  // which of the last inputs, if any
         if (dso && r >= 0 && r < K - 1) {
-          float2 e[2];
-          pairs_of(load4<T, VEC>(dso + r * g.dstate_out.step, p.have, true), e);
-          o[0] = __fadd2_rn(o[0], e[0]);
-          o[1] = __fadd2_rn(o[1], e[1]);
+          float2 e[P];
+          pairs_of(load_channels<T, V, VEC>(dso + r * g.dstate_out.step, p.have, true), e);
+#pragma unroll
+          for (int i = 0; i < P; ++i) o[i] = __fadd2_rn(o[i], e[i]);
         }
         if (q >= 0)
-          store4<T, VEC>(dx + q * g.dx.step, p.have, o);
+          store_channels<T, VEC>(dx + q * g.dx.step, p.have, o);
         else if (dsi)
-          store4<T, VEC>(dsi + (q + K - 1) * g.dstate_in.step, p.have, o);
+          store_channels<T, VEC>(dsi + (q + K - 1) * g.dstate_in.step, p.have, o);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) {
         xw[j][i] = xw[U + j][i];
@@ -279,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 4 : K <= 5 ? 3 : 2)
   // partial sums of this run: [set][row of set, run][K + 1][D]
   float* out = part + (p.row * d.runs + p.run) * (K + 1) * d.D + p.c;
 #pragma unroll
-  for (int k = 0; k <= K; ++k) store4<float, VEC>(out + (int64_t)k * d.D, p.have, k < K ? dw[k < K ? k : K - 1] : db);
+  for (int k = 0; k <= K; ++k) store_channels<float, VEC>(out + (int64_t)k * d.D, p.have, k < K ? dw[k < K ? k : K - 1] : db);
 }
 
 struct SumOuts {
@@ -323,18 +334,20 @@ __global__ void __launch_bounds__(32 * G)
   }
 }
 
-// Steps of one run: whole rows where there are rows enough for `blocks` blocks an SM (two
-// waves of what stays there), else as many runs as give that, but not under 16 steps
-// (and so never under the K - 1 steps by which neighbouring runs overlap).  At most 256,
-// so that the backward pass's sums have two stages.
-ConvDims conv_dims(const zo_conv_args& a, int blocks) {
+// Steps of one run.  Neighbouring runs both read K - 1 steps and the backward pass sums over
+// runs, so they should be long; and all blocks together should nearly fill a whole number of
+// waves, `held` blocks an SM each: two waves where that leaves runs of 24 steps, else one, and
+// 16 steps at least.  At most 256 steps, so that the backward pass's sums have two stages.
+ConvDims conv_dims(const zo_conv_args& a, int V, int held) {
   ConvDims d;
   d.T = a.seq;
   d.D = a.channels;
   d.rows_per_set = a.rows / a.sets;
   d.ctiles = (int)ceil_div(ceil_div(a.channels, V), kThreads);
-  const int64_t want = ceil_div(blocks * kBlockSMs, (int64_t)d.ctiles * a.rows);
-  int64_t run = ceil_div(a.seq, want);
+  const int64_t per_run = (int64_t)d.ctiles * a.rows, wave = held * kBlockSMs;
+  auto steps = [&](int64_t blocks) { return ceil_div(a.seq, blocks < per_run ? 1 : blocks / per_run); };
+  int64_t run = steps(2 * wave);
+  if (run < 24) run = steps(wave);
   run = run < 16 ? 16 : run > 256 ? 256 : run;
   d.run = (int)run;
   d.runs = (int)ceil_div(a.seq, run);
@@ -343,15 +356,16 @@ ConvDims conv_dims(const zo_conv_args& a, int blocks) {
     d.params = d.params && p->stride % V == 0 && reinterpret_cast<uintptr_t>(p->ptr) % 16 == 0;
   return d;
 }
-ConvDims forward_dims(const zo_conv_args& a) { return conv_dims(a, 10); }
-ConvDims backward_dims(const zo_conv_args& a) { return conv_dims(a, 8); }
+// Channels a thread: with eight, the forward of 8 x 2048 x 4096 takes 83 us instead of 70.
+constexpr int kChannels = 4;
+ConvDims backward_dims(const zo_conv_args& a) { return conv_dims(a, kChannels, held_backward(a.taps)); }
 
 template <class T, int K, bool VEC>
 cudaError_t run_conv(const zo_conv_args& a, cudaStream_t st) {
-  const ConvDims d = forward_dims(a);
+  const ConvDims d = conv_dims(a, kChannels, held_forward(K));
   const int64_t blocks = (int64_t)d.ctiles * d.runs * a.rows;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  conv_kernel<T, K, 8, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(a, d);
+  conv_kernel<T, K, kChannels, 4, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(a, d);
   count_launch();
   return cudaGetLastError();
 }
@@ -362,7 +376,7 @@ cudaError_t run_conv_backward(const zo_conv_args& a, const zo_conv_grads& g, flo
   const ConvDims d = backward_dims(a);
   const int64_t blocks = (int64_t)d.ctiles * d.runs * a.rows;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  conv_backward_kernel<T, K, 4, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(a, g, d, ws);
+  conv_backward_kernel<T, K, kChannels, 4, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(a, g, d, ws);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -385,8 +399,8 @@ cudaError_t by_taps(int taps, F&& f) {
   }
 }
 
-// Whether four channels of all of these can be accessed together.
-bool vectors(std::initializer_list<const zo_tensor*> tensors, int elem, int channels) {
+// Whether V channels of all of these can be accessed together.
+bool vectors(std::initializer_list<const zo_tensor*> tensors, int elem, int channels, int V) {
   for (const zo_tensor* t : tensors)
     if (vec_width(*t, elem, channels, V) != V) return false;
   return true;
@@ -394,7 +408,7 @@ bool vectors(std::initializer_list<const zo_tensor*> tensors, int elem, int chan
 
 template <class T>
 cudaError_t conv_typed(const zo_conv_args& a, cudaStream_t st) {
-  const bool vec = vectors({&a.x, &a.out, &a.state_in, &a.state_out}, sizeof(T), a.channels);
+  const bool vec = vectors({&a.x, &a.out, &a.state_in, &a.state_out}, sizeof(T), a.channels, kChannels);
   return by_taps(a.taps, [&](auto k) {
     return vec ? run_conv<T, decltype(k)::value, true>(a, st) : run_conv<T, decltype(k)::value, false>(a, st);
   });
@@ -403,7 +417,7 @@ cudaError_t conv_typed(const zo_conv_args& a, cudaStream_t st) {
 template <class T>
 cudaError_t conv_backward_typed(const zo_conv_args& a, const zo_conv_grads& g, float* ws,
                                 cudaStream_t st) {
-  const bool vec = vectors({&a.x, &a.state_in, &g.dout, &g.dx, &g.dstate_out, &g.dstate_in}, sizeof(T), a.channels);
+  const bool vec = vectors({&a.x, &a.state_in, &g.dout, &g.dx, &g.dstate_out, &g.dstate_in}, sizeof(T), a.channels, kChannels);
   return by_taps(a.taps, [&](auto k) {
     return vec ? run_conv_backward<T, decltype(k)::value, true>(a, g, ws, st)
                : run_conv_backward<T, decltype(k)::value, false>(a, g, ws, st);
@@ -426,7 +440,7 @@ cudaError_t launch_sum_parts(const float* part, int sets, int64_t parts, int64_t
     const int ns = sets - s0 < 65535 ? sets - s0 : 65535;
     const dim3 grid((unsigned)bx, (unsigned)ns);
     const float* p = part + (int64_t)s0 * parts * n;
-    if (parts > 64 && bx * ns < kBlockSMs)  // more threads a value where there are few values
+    if (parts > 64 && (bx * ns < kBlockSMs || parts > 256))  // more threads a value
       sum_parts_kernel<32><<<grid, 1024, 0, st>>>(p, parts, n, o);
     else
       sum_parts_kernel<8><<<grid, 256, 0, st>>>(p, parts, n, o);
