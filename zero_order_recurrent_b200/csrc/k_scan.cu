@@ -706,10 +706,13 @@ constexpr int kSub = 2;      // steps whose states and decays are in registers t
 constexpr int kBlock = 4;    // steps between states kept in shared memory
 constexpr int kFlush = 64;   // chunks after which the parameters' sums are put away
 
+// Warps of a block at most: 128 channels.
 template <int LN>
+constexpr int kBackWarps = LN >= 4 ? 4 : LN;
+
+template <int LN, int WARPS>
 struct BackTile {
-  static constexpr int kWarps = LN >= 4 ? 4 : LN;          // 128 channels a block, or less
-  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kWarps = WARPS, kThreads = 32 * kWarps;
   static constexpr int kWarpChannels = 128 / LN, kChannels = kWarps * kWarpChannels;
   static constexpr int NP = 4 * LN, kMid = kChunk / kBlock - 1;
   alignas(16) float d[kChunk][kChannels], u[kChunk][kChannels], dy[kChunk][kChannels];
@@ -737,10 +740,10 @@ struct BackSums {
 // comes back through them.  The exponentials are so done 2.25 times, which costs less than to
 // keep every state in memory.  More steps in registers, or all states before kSub steps in
 // shared memory, leave two blocks an SM instead of three.
-template <class T, int LN>
-__global__ void __launch_bounds__(BackTile<LN>::kThreads, LN >= 4 ? 3 : 3 * 4 / LN / 2)
+template <class T, int LN, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, LN >= 4 ? 12 / WARPS : 6 / WARPS)
     scan_backward_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, Parts parts, BackSums sums, bool vec) {
-  using S = BackTile<LN>;
+  using S = BackTile<LN, WARPS>;
   extern __shared__ __align__(16) unsigned char smem[];
   S& sh = *reinterpret_cast<S*>(smem);
   const unsigned tiles = d.tiles * d.G;
@@ -1142,7 +1145,7 @@ int lanes_per_channel(int N) {
 // them) runs at about min(w, 1) of the special function unit's rate; in parts the
 // exponentials come twice (37 instead of 21 results a value).  So time is divided
 // where there are under half as many warps as schedulers, into as many parts as
-// make four blocks an SM at most (which is what stays there), of 64 steps at least.
+// make four blocks an SM at most (which is what stays there), of 32 steps at least.
 struct ScanPlan {
   int warps, tiles, parts, steps;
 };
@@ -1156,7 +1159,7 @@ ScanPlan scan_plan(const zo_scan_args& a) {
   const int64_t blocks = (int64_t)p.tiles * a.groups * a.rows;
   int64_t n = all * 2 < 4 * kBlockSMs ? 4 * kBlockSMs / blocks : 1;
   int64_t steps = ceil_div(ceil_div(a.seq, n), kChunk) * kChunk;
-  if (n > 1 && steps < 64) steps = 64;
+  if (n > 1 && steps < 32) steps = 32;
   p.parts = (int)ceil_div(a.seq, steps);
   p.steps = p.parts > 1 ? (int)steps : (int)(ceil_div(a.seq, kChunk) * kChunk);
   return p;
@@ -1220,19 +1223,22 @@ cudaError_t run_scan_step(const zo_scan_args& a, cudaStream_t st) {
 
 // The backward pass's division of time: as scan_plan, for its own blocks.
 struct BackPlan {
-  int tiles, parts, steps, flushes;
+  int warps, tiles, parts, steps, flushes;
   int64_t bc, param, state, sum;  // floats of workspace
 };
 template <int LN>
 BackPlan back_plan(const zo_scan_args& a) {
-  using S = BackTile<LN>;
   BackPlan p;
-  p.tiles = (int)ceil_div(a.channels / a.groups, S::kChannels);
+  // Blocks of several warps share B and C and leave fewer partial sums; blocks of one where the
+  // others would leave a fifth of their warps without channels.
+  const int64_t w = ceil_div(a.channels / a.groups, 128 / LN), most = kBackWarps<LN>;
+  p.warps = 5 * ceil_div(w, most) * most > 6 * w ? 1 : (int)most;
+  p.tiles = (int)ceil_div(w, p.warps);
   const int64_t blocks = (int64_t)p.tiles * a.groups * a.rows;
-  const int64_t room = 12 / S::kWarps * kBlockSMs;  // blocks that the SMs hold
+  const int64_t room = (LN >= 4 ? 12 : 6) / p.warps * kBlockSMs;  // blocks that the SMs hold
   int64_t n = blocks * 2 < room ? room / blocks : 1;
   int64_t steps = ceil_div(ceil_div(a.seq, n), kChunk) * kChunk;
-  if (n > 1 && steps < 64) steps = 64;
+  if (n > 1 && steps < 32) steps = 32;
   p.parts = (int)ceil_div(a.seq, steps);
   p.steps = (int)steps;
   p.flushes = (int)ceil_div(steps / kChunk, kFlush);
@@ -1247,7 +1253,6 @@ BackPlan back_plan(const zo_scan_args& a) {
 template <class T, int LN, int S, int LC>
 cudaError_t run_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, float* ws,
                               cudaStream_t st) {
-  using B = BackTile<LN>;
   const BackPlan p = back_plan<LN>(a);
   ScanDims d = scan_dims<LN>(a);
   d.tiles = p.tiles;
@@ -1276,10 +1281,16 @@ cudaError_t run_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, flo
   bool vec = true;
   for (const zo_tensor* t : {&a.u, &a.delta, &a.z, &g.dout})
     vec = vec && vec_width(*t, sizeof(T), d.Dg, 4) == 4;
-  if ((e = allow_shared(scan_backward_kernel<T, LN>, (int)sizeof(B))) != cudaSuccess) return e;
-  scan_backward_kernel<T, LN><<<(unsigned)blocks, B::kThreads, sizeof(B), st>>>(a, g, d, parts, sums, vec);
-  count_launch();
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  auto launch = [&](auto warps) {
+    constexpr int W = decltype(warps)::value, kSmem = (int)sizeof(BackTile<LN, W>);
+    const cudaError_t r = allow_shared(scan_backward_kernel<T, LN, W>, kSmem);
+    if (r != cudaSuccess) return r;
+    scan_backward_kernel<T, LN, W><<<(unsigned)blocks, 32 * W, kSmem, st>>>(a, g, d, parts, sums, vec);
+    count_launch();
+    return cudaGetLastError();
+  };
+  e = p.warps == 1 ? launch(std::integral_constant<int, 1>()) : launch(std::integral_constant<int, kBackWarps<LN>>());
+  if (e != cudaSuccess) return e;
   sum_bc_kernel<T><<<(unsigned)ceil_div(bc, 256), 256, 0, st>>>(a, g, d, sums.bc);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
