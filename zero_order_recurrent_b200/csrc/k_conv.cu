@@ -7,6 +7,9 @@
 // neighbouring channels and walks a run of steps with the window in registers, in
 // pairs of channels for the packed fp32 instructions, so x is read once per run plus
 // K - 1 steps of overlap; the next U steps are on their way while U are computed.
+// Measured at 8 rows x 2048 steps x 4096 channels, K = 4, bf16: forward 68 us (4.0 TB/s),
+// backward 167 us (2.4 TB/s).  Neither wider accesses nor more steps ahead nor more
+// blocks an SM change the forward by more than a tenth.
 #include <initializer_list>
 #include <type_traits>
 

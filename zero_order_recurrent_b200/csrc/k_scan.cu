@@ -218,14 +218,18 @@ struct BC {
 // Bound: the special function unit, 16 results a clock and SM.  A value with 16
 // states takes 16 exponentials and 5 for softplus and silu, so 21 / 16 clocks; its
 // 8 bytes in bf16 take 0.34 clocks of an SM's share of the memory.  The 16
-// exponentials of one step are independent, so a warp a scheduler nearly fills the
-// unit.  Fewer lanes a state (four states a lane) make more warps, but were bound
-// by shared-memory accesses and issue: 2.5 times the instructions a value.
+// exponentials of one step are independent.  Four states a lane and four warps along
+// time, each keeping its decays in registers for a second run, make more warps without parts,
+// but took 7.6 instructions a value, which bound them, against 3.6 here.
 //
 // Where rows and channels are too few for the SMs, time is divided as well: LOCAL
 // runs each part but the last from the state 0, scan_join_kernel passes the states
 // on from part to part, and then all parts run from the states they start with.
 // That takes the exponentials twice.
+//
+// Measured: 4096 rows x 10 steps x 1024 channels with states in and out 343 us (2.6 TB/s; by
+// the unit's count 196); 1 row x 16384 steps x 2048 channels in 37 parts 397 us (by its count
+// 276, the unit 60 to 70% busy).
 //
 // A block takes `rows` rows of one set one after the other.
 constexpr int kAhead = 4;
@@ -461,7 +465,8 @@ __global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims
 
 // One token.  A thread holds four states of a channel and walks RG rows of a
 // set, so that A is read once for them; all its loads are issued before the first result is
-// waited for.  Bound: the states, read and written.  WIDE: states, B and C four at a time.
+// waited for.  Bound: the states, read and written: 512 rows x 4096 channels take 75 us, 3.8 TB/s.
+// WIDE: states, B and C four at a time.
 template <class T, int LN, int RG, bool WIDE>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, ScanDims d, int64_t groups) {
   const int64_t nb = ((int64_t)d.D * LN + kThreads - 1) / kThreads;  // blocks of a row
@@ -739,7 +744,12 @@ struct BackSums {
 // blocks and kSub steps at a time, states and decays are run again into registers and the carry
 // comes back through them.  The exponentials are so done 2.25 times, which costs less than to
 // keep every state in memory.  More steps in registers, or all states before kSub steps in
-// shared memory, leave two blocks an SM instead of three.
+// shared memory, leave two blocks an SM instead of three (576 against 561 us, 649 against 561).
+//
+// Bound: issue, at 570 instructions for 32 channels, 16 states and a step, half of the slots
+// used with three warps a scheduler; the multiply-add pipe and the special function unit (43 of its
+// results a value) follow.  4 rows x 2048 steps x 2048 channels: 561 us, and 124 us for the
+// carries, against 42 us of memory traffic for the whole training step.
 template <class T, int LN, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, LN >= 4 ? 12 / WARPS : 6 / WARPS)
     scan_backward_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, Parts parts, BackSums sums, bool vec) {
@@ -1141,11 +1151,12 @@ int lanes_per_channel(int N) {
 }
 
 // Warps of a block (at most four, and no more than a group's channels fill),
-// and the parts of time.  One pass over time with w warps a scheduler (592 of
-// them) runs at about min(w, 1) of the special function unit's rate; in parts the
-// exponentials come twice (37 instead of 21 results a value).  So time is divided
-// where there are under half as many warps as schedulers, into as many parts as
-// make four blocks an SM at most (which is what stays there), of 32 steps at least.
+// and the parts of time.  A warp alone on its scheduler keeps the special function
+// unit busy a third of the time, and in parts the exponentials come twice (37 instead of
+// 21 results a value), so time is divided where there are under 4/3 warps for each of the 592
+// schedulers, into as many parts as make four blocks an SM at most (which is what stays there),
+// of 32 steps at least.  2048 steps of 2048 channels in one pass and in parts: 2 rows (128
+// warps) 452 and 131 us, 4 rows 455 and 223, 8 rows 457 and 408, 12 rows 578 and 543.
 struct ScanPlan {
   int warps, tiles, parts, steps;
 };
@@ -1157,7 +1168,7 @@ ScanPlan scan_plan(const zo_scan_args& a) {
   p.tiles = (int)ceil_div(w, p.warps);
   const int64_t all = w * a.groups * a.rows;
   const int64_t blocks = (int64_t)p.tiles * a.groups * a.rows;
-  int64_t n = all * 2 < 4 * kBlockSMs ? 4 * kBlockSMs / blocks : 1;
+  int64_t n = 3 * all < 16 * kBlockSMs ? 4 * kBlockSMs / blocks : 1;
   int64_t steps = ceil_div(ceil_div(a.seq, n), kChunk) * kChunk;
   if (n > 1 && steps < 32) steps = 32;
   p.parts = (int)ceil_div(a.seq, steps);
@@ -1221,7 +1232,9 @@ cudaError_t run_scan_step(const zo_scan_args& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// The backward pass's division of time: as scan_plan, for its own blocks.
+// The backward pass's division of time: parts, which cost a pass over the carries, wherever the
+// SMs hold twice the blocks.  2048 steps of 2048 channels in one pass and in parts: 2 rows
+// (32 blocks) 2050 and 328 us, 8 rows 2073 and 1255, 12 rows 2518 and 1859.
 struct BackPlan {
   int warps, tiles, parts, steps, flushes;
   int64_t bc, param, state, sum;  // floats of workspace
