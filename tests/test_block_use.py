@@ -508,3 +508,61 @@ def test_offsets_beyond_32_bits():
     zo.zo_scan_step(f[:, 0], f[:, 1], A, B[:, 0].float(), B[:, 1].float(), cache, ya)
     zo.zo_scan_step(f[:, 0], f[:, 1], A, B[:, 0].float(), B[:, 1].float(), h, yb)
     assert torch.equal(ya, yb) and torch.equal(cache, h)
+
+
+@gpu
+def test_shared_parameters_and_broadcast_inputs():
+    """A and the taps shared by all sets while other parameters differ; B and C of one row for all."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+
+    def r(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    R, T, D, N, S, K = 6, 20, 24, 8, 3, 4
+    u, dl, dout = r(R, T, D), r(R, T, D), r(R, T, D)
+    A, bias, skip = -torch.rand(D, N, generator=g, device="cuda"), r(S, D), r(D)
+    B, C = r(1, T, 1, N).expand(R, T, 1, N), r(R, 1, 1, N).expand(R, T, 1, N)
+    kept = torch.empty(zo.zo_scan_checkpoint_shape(u.shape, N), device="cuda")
+
+    def both(A, skip, B, C):
+        out, du, dd = (torch.empty_like(u) for _ in range(3))
+        dA, ds, db = torch.empty(S, D, N, device="cuda"), torch.empty(S, D, device="cuda"), torch.empty(S, D, device="cuda")
+        dB, dC = (torch.empty(R, T, 1, N, device="cuda") for _ in range(2))
+        zo.zo_scan(u, dl, A, B, C, out, skip=skip, delta_bias=bias, checkpoints=kept)
+        zo.zo_scan_backward(u, dl, A, B, C, dout, kept, du, dd, dA, dB, dC, skip=skip, dskip=ds, delta_bias=bias,
+                            ddelta_bias=db)
+        return out, du, dd, dA, ds, db, dB, dC
+    for a, b in zip(both(A, skip, B, C), both(A.expand(S, D, N).contiguous(), skip.expand(S, D).contiguous(),
+                                              B.contiguous(), C.contiguous())):
+        assert torch.equal(a, b)
+    w, cb, a, b = r(K, D), r(S, D), torch.empty_like(u), torch.empty_like(u)
+    zo.zo_conv(u, w, a, bias=cb)
+    zo.zo_conv(u, w.expand(S, K, D).contiguous(), b, bias=cb)
+    assert torch.equal(a, b)
+    x, o = u.reshape(-1, D), dl.reshape(-1, D)
+    zo.zo_block_norm(x, x_out=a.view(-1, D), o=o, w_post=skip, scale=cb)
+    zo.zo_block_norm(x, x_out=b.view(-1, D), o=o, w_post=skip.expand(S, D).contiguous(), scale=cb)
+    assert torch.equal(a, b)
+
+
+@gpu
+def test_steps_without_state_out_leave_the_state():
+    R, D, N, K = 3, 16, 8, 4
+    u, st = torch.randn(R, D, device="cuda"), torch.randn(R, D, N, device="cuda")
+    A, B = -torch.rand(D, N, device="cuda"), torch.randn(R, 1, N, device="cuda")
+    out, want, kept = torch.empty_like(u), torch.empty_like(u), st.clone()
+    zo.zo_scan_step(u, u, A, B, B, st.clone(), want)
+    t, bc = (lambda p: block._Tensor(p.data_ptr(), D, 0)), block._Tensor(B.data_ptr(), N, 0)
+    a = block.ScanArgs(R, 1, D, 1, N, 1, zo.ZO_DTYPE_FP32, zo.ZO_SCAN_SOFTPLUS, t(u), t(u), t(out), block._Tensor(), bc, bc,
+                       block._F32(A.data_ptr(), 0))
+    a.state_in = block._F32(st.data_ptr(), D * N)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert zo.load_library().zo_scan_step(a, stream) == zo.ZO_OK
+    assert torch.equal(out, want) and torch.equal(st, kept)
+    win, w = torch.randn(R, K - 1, D, device="cuda"), torch.randn(K, D, device="cuda")
+    kept = win.clone()
+    zo.zo_conv_step(u, w, win.clone(), want)
+    a = block.ConvArgs(R, 1, D, K, 1, zo.ZO_DTYPE_FP32, zo.ZO_CONV_SILU, t(u), t(out), block._F32(w.data_ptr(), 0))
+    a.state_in = block._Tensor(win.data_ptr(), (K - 1) * D, D)
+    assert zo.load_library().zo_conv_step(a, stream) == zo.ZO_OK
+    assert torch.equal(out, want) and torch.equal(win, kept)
