@@ -90,7 +90,6 @@ __device__ __forceinline__ float2 softplus_2(float2 x) {
   const float2 l = __ffma2_rn(s2, __fmul2_rn(w, p), s2);
   return __fadd2_rn(make_float2(relu_nan(x.x), relu_nan(x.y)), l);
 }
-__device__ __forceinline__ float softplus_f(float x) { return softplus_2(two(x)).x; }
 
 template <int LN>
 __device__ __forceinline__ float sum_lanes(float v) {
@@ -328,6 +327,8 @@ __global__ void __launch_bounds__(128, 4)
       else if (a.state_in.ptr)
         load_pairs<S>(a.state_in.ptr + row * a.state_in.stride + c * d.N, n0, d.N, wide, h);
     }
+    if (!LOCAL && more && a.state_in.ptr && n0 < d.N)  // on its way while this row is computed
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.state_in.ptr + (row + 1) * a.state_in.stride + c * d.N + n0));
     T* out = LOCAL ? nullptr : static_cast<T*>(a.out.ptr) + row * a.out.row + tb * a.out.step + c;
     int t = tb;
     for (; t < end; t += kTile) {
@@ -465,72 +466,79 @@ __global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims
 
 // One token.  A thread holds four states of a channel and walks RG rows of a
 // set, so that A is read once for them; all its loads are issued before the first result is
-// waited for.  Bound: the states, read and written: 512 rows x 4096 channels take 75 us, 3.8 TB/s.
-// WIDE: states, B and C four at a time.
-template <class T, int LN, int RG, bool WIDE>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, ScanDims d, int64_t groups) {
-  const int64_t nb = ((int64_t)d.D * LN + kThreads - 1) / kThreads;  // blocks of a row
-  const int64_t i = blockIdx.x % nb * kThreads + threadIdx.x;       // (channel, lane)
+// waited for.  Bound: the states, read and written: 512 rows x 4096 channels take 60 us, 4.8 TB/s.
+// HOW: 2 - every lane has four states, which, like those of A, B and C, are on 16 (8) bytes;
+// 1 - so, but lanes behind the last state have none; 0 - states one at a time.
+template <class T, int LN, int RG, int HOW>
+__global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, ScanDims d, unsigned groups) {
+  const unsigned nb = ((unsigned)d.D * LN + kThreads - 1) / kThreads;  // blocks of a row
+  const unsigned i = blockIdx.x % nb * kThreads + threadIdx.x;        // (channel, lane)
   const int q = (int)(i % LN), n0 = q * 4;
-  const bool on = i / LN < d.D;
-  const int64_t c = on ? i / LN : 0;
-  const int64_t first = blockIdx.x / nb * RG, set = first / groups;
-  const int64_t r0 = set * d.rows_per_set + first % groups;
-  const int have = (int)(d.rows_per_set - first % groups);  // rows of the set from r0 on
-  const int64_t g = c / d.Dg;
-  auto four = [&](auto* p, int n, bool there) {  // p[n ..], zeros from N on
+  const bool on = i / LN < (unsigned)d.D;
+  const int c = on ? (int)(i / LN) : 0;
+  const unsigned first = blockIdx.x / nb * RG, set = first / groups, in_set = first % groups;
+  const int have = d.rows_per_set - (int)in_set;  // rows of the set from the first on
+  const int64_t r0 = (int64_t)set * d.rows_per_set + in_set;
+  const int64_t g = c / d.Dg, cn = (int64_t)c * d.N;
+  auto four = [&](auto* p, auto& x) {  // p[n0 ..], zeros from N on
     using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
-    if constexpr (WIDE) {
-      return load_if<E, 4>(p + n, there && n < d.N);
+    if constexpr (HOW == 2) {
+      x = *reinterpret_cast<const Vec<E, 4>*>(p + n0);
+    } else if constexpr (HOW == 1) {
+      x = load_if<E, 4>(p + n0, n0 < d.N);
     } else {
-      Vec<E, 4> x;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x.v[j] = load_if<E, 1>(p + n + j, there && n + j < d.N).v[0];
-      return x;
+      for (int j = 0; j < 4; ++j) x.v[j] = load_if<E, 1>(p + n0 + j, n0 + j < d.N).v[0];
     }
   };
-  Vec<float, 4> h[RG];
+  Vec<float, 4> A, h[RG];
   Vec<T, 4> B[RG], C[RG];
   T u[RG], dl[RG], z[RG];
+  const T* pz = static_cast<const T*>(a.z.ptr ? a.z.ptr : a.u.ptr);
+  const int64_t z_row = a.z.ptr ? a.z.row : a.u.row;
 #pragma unroll
   for (int k = 0; k < RG; ++k) {
-    const int64_t row = r0 + k;
-    const bool there = on && k < have;
-    h[k] = four(static_cast<const float*>(a.state_in.ptr) + row * a.state_in.stride + c * d.N, n0, there);
-    B[k] = four(static_cast<const T*>(a.B.ptr) + row * a.B.row + g * d.N, n0, there);
-    C[k] = four(static_cast<const T*>(a.C.ptr) + row * a.C.row + g * d.N, n0, there);
-    u[k] = load_if<T, 1>(static_cast<const T*>(a.u.ptr) + row * a.u.row + c, there).v[0];
-    dl[k] = load_if<T, 1>(static_cast<const T*>(a.delta.ptr) + row * a.delta.row + c, there).v[0];
-    z[k] = load_if<T, 1>(static_cast<const T*>(a.z.ptr) + row * a.z.row + c, there && a.z.ptr).v[0];
+    const int64_t row = r0 + (k < have ? k : have - 1);  // the last row again behind it
+    four(static_cast<const float*>(a.state_in.ptr) + row * a.state_in.stride + cn, h[k]);
+    four(static_cast<const T*>(a.B.ptr) + row * a.B.row + g * d.N, B[k]);
+    four(static_cast<const T*>(a.C.ptr) + row * a.C.row + g * d.N, C[k]);
+    u[k] = static_cast<const T*>(a.u.ptr)[row * a.u.row + c];
+    dl[k] = static_cast<const T*>(a.delta.ptr)[row * a.delta.row + c];
+    z[k] = pz[row * z_row + c];
   }
-  float A[4];
-  load_states(a.A.ptr + set * a.A.stride + c * d.N, n0, d.N, A);
-  const float2 A2[2] = {make_float2(rate(A[0]), rate(A[1])), make_float2(rate(A[2]), rate(A[3]))};
+  four(static_cast<const float*>(a.A.ptr) + set * a.A.stride + cn, A);
+  const float2 A2[2] = {make_float2(rate(A.v[0]), rate(A.v[1])), make_float2(rate(A.v[2]), rate(A.v[3]))};
   const float skip = a.skip.ptr ? a.skip.ptr[set * a.skip.stride + c] : 0.f;
   const float bias = a.delta_bias.ptr ? a.delta_bias.ptr[set * a.delta_bias.stride + c] : 0.f;
 #pragma unroll
-  for (int k = 0; k < RG; ++k) {
-    if (k >= have) break;
-    const int64_t row = r0 + k;
-    const float uk = to_f(u[k]);
-    float dt = to_f(dl[k]) + bias;
-    if (a.flags & ZO_SCAN_SOFTPLUS) dt = softplus_f(dt);
-    const float2 x = two(dt * uk);
-    float2 y = two(0.f);
-    float f[4];
+  for (int k0 = 0; k0 < RG; k0 += 2) {  // two rows at a time where one channel's work is done
+    constexpr int P = RG > 1 ? 2 : 1;
+    if (k0 >= have) break;
+    const int k1 = k0 + P - 1;
+    const float2 uu = make_float2(to_f(u[k0]), to_f(u[k1]));
+    float2 dt = __fadd2_rn(make_float2(to_f(dl[k0]), to_f(dl[k1])), two(bias));
+    if (a.flags & ZO_SCAN_SOFTPLUS) dt = softplus_2(dt);
+    const float2 xx = __fmul2_rn(dt, uu);
+    const float2 gate = a.z.ptr ? silu_2(make_float2(to_f(z[k0]), to_f(z[k1]))) : two(1.f);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const float2 v = __ffma2_rn(exp2_2(__fmul2_rn(two(dt), A2[p])), make_float2(h[k].v[2 * p], h[k].v[2 * p + 1]),
-                                  __fmul2_rn(x, make_float2(to_f(B[k].v[2 * p]), to_f(B[k].v[2 * p + 1]))));
-      y = __ffma2_rn(make_float2(to_f(C[k].v[2 * p]), to_f(C[k].v[2 * p + 1])), v, y);
-      f[2 * p] = v.x, f[2 * p + 1] = v.y;
-    }
-    if (on && a.state_out.ptr)
-      store_states4<WIDE>(a.state_out.ptr + row * a.state_out.stride + c * d.N, n0, d.N, f);
-    float out = fmaf(skip, uk, sum_lanes<LN>(y.x + y.y));
-    if (on && q == 0) {
-      if (a.z.ptr) out *= silu_2(two(to_f(z[k]))).x;
-      static_cast<T*>(a.out.ptr)[row * a.out.row + c] = from_f<T>(out);
+    for (int e = 0; e < P; ++e) {
+      const int k = k0 + e;
+      if (k >= have) break;
+      const float2 x = two(e ? xx.y : xx.x), d2 = two(e ? dt.y : dt.x);
+      float2 y = two(0.f);
+      float f[4];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const float2 v = __ffma2_rn(exp2_2(__fmul2_rn(d2, A2[p])), make_float2(h[k].v[2 * p], h[k].v[2 * p + 1]),
+                                    __fmul2_rn(x, make_float2(to_f(B[k].v[2 * p]), to_f(B[k].v[2 * p + 1]))));
+        y = __ffma2_rn(make_float2(to_f(C[k].v[2 * p]), to_f(C[k].v[2 * p + 1])), v, y);
+        f[2 * p] = v.x, f[2 * p + 1] = v.y;
+      }
+      const int64_t row = r0 + k;
+      if (on && a.state_out.ptr)
+        store_states4<HOW != 0>(a.state_out.ptr + row * a.state_out.stride + cn, n0, d.N, f);
+      const float out = fmaf(skip, e ? uu.y : uu.x, sum_lanes<LN>(y.x + y.y)) * (e ? gate.y : gate.x);
+      if (on && q == 0) static_cast<T*>(a.out.ptr)[row * a.out.row + c] = from_f<T>(out);
     }
   }
 }
@@ -1219,15 +1227,18 @@ cudaError_t run_scan_step(const zo_scan_args& a, cudaStream_t st) {
   const ScanDims d = scan_dims<LN>(a);
   const int64_t groups = ceil_div(d.rows_per_set, RG) * RG;  // rows of a set, whole groups
   const int64_t blocks = ceil_div((int64_t)d.D * LN, kThreads) * (groups / RG) * a.sets;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (blocks > INT32_MAX || (int64_t)d.D * LN > INT32_MAX || groups * a.sets > UINT32_MAX)
+    return cudaErrorInvalidConfiguration;
   bool wide = d.N % 4 == 0;
-  for (const zo_f32* p : {&a.state_in, &a.state_out})
+  for (const zo_f32* p : {&a.A, &a.state_in, &a.state_out})
     wide = wide && p->stride % 4 == 0 && reinterpret_cast<uintptr_t>(p->ptr) % 16 == 0;
   for (const zo_tensor* t : {&a.B, &a.C}) wide = wide && vec_width(*t, sizeof(T), 4, 4) == 4;
-  if (wide)
-    scan_step_kernel<T, LN, RG, true><<<(unsigned)blocks, kThreads, 0, st>>>(a, d, groups);
+  if (wide && d.N == 4 * LN)
+    scan_step_kernel<T, LN, RG, 2><<<(unsigned)blocks, kThreads, 0, st>>>(a, d, (unsigned)groups);
+  else if (wide)
+    scan_step_kernel<T, LN, RG, 1><<<(unsigned)blocks, kThreads, 0, st>>>(a, d, (unsigned)groups);
   else
-    scan_step_kernel<T, LN, RG, false><<<(unsigned)blocks, kThreads, 0, st>>>(a, d, groups);
+    scan_step_kernel<T, LN, RG, 0><<<(unsigned)blocks, kThreads, 0, st>>>(a, d, (unsigned)groups);
   count_launch();
   return cudaGetLastError();
 }
