@@ -186,6 +186,7 @@ SCAN = [  # R, T, D, G, N, S, dtype, ragged, state, gate, softplus, pad
     (5, 2, 96, 1, 16, 5, "bf16", True, True, True, True, True),
     (1, 2500, 16, 1, 16, 1, "f32", None, True, True, True, False),
     (230, 1100, 8, 1, 16, 2, "f32", True, False, True, True, False),
+    (650, 40, 8, 1, 16, 2, "f32", True, True, False, True, False),
     (6000, 5, 8, 1, 16, 3, "bf16", True, True, True, True, False),
     (2600, 40, 40, 1, 8, 1, "f16", True, False, True, True, False),
 ]

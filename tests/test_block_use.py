@@ -141,6 +141,27 @@ def test_norm_refuses_more():
     assert lib.zo_block_norm_backward(a, block.NormGrads(**good), P, need - 1, None) == zo.ZO_ERR_INVALID_ARG
 
 
+def test_workspaces_of_all_sizes():
+    """The plans behind the workspaces, over rows, steps, channels, groups and states: sizes that
+    every block arithmetic has to get through, without a device."""
+    lib = zo.load_library()
+    for rows in (1, 2, 7, 100, 591, 592, 593, 650, 788, 789, 790, 5000, 2 ** 20):
+        for seq in (1, 15, 16, 17, 33, 64, 1000, 2 ** 20, 2 ** 30):
+            for channels, groups in ((1, 1), (8, 1), (32, 1), (33, 1), (96, 2), (520, 4), (4096, 1), (2 ** 20, 8)):
+                if rows * seq * channels > 2 ** 44:
+                    continue
+                for states in (1, 4, 5, 8, 16, 17, 64, 128):
+                    a = scan_args(rows=rows, seq=seq, channels=channels, groups=groups, states=states)
+                    n = lib.zo_scan_workspace(a)
+                    parts = n // (4 * rows * channels * (states + 1))
+                    assert n == parts * 4 * rows * channels * (states + 1) and (parts == 0 or 2 <= parts <= seq)
+                    assert lib.zo_scan_backward_workspace(a) > 4 * rows * channels * states
+                a = conv_args(rows=rows, seq=seq, channels=channels)
+                assert lib.zo_conv_backward_workspace(a) >= 4 * rows * channels * 5
+            if channels <= 16384:
+                assert lib.zo_block_norm_backward_workspace(norm_args(rows=rows, channels=channels)) > 0
+
+
 def test_calls_without_a_device_report_it():
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")

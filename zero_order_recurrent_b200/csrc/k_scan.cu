@@ -1177,6 +1177,7 @@ ScanPlan scan_plan(const zo_scan_args& a) {
   const int64_t all = w * a.groups * a.rows;
   const int64_t blocks = (int64_t)p.tiles * a.groups * a.rows;
   int64_t n = 3 * all < 16 * kBlockSMs ? 4 * kBlockSMs / blocks : 1;
+  if (n < 1) n = 1;  // blocks of one warp
   int64_t steps = ceil_div(ceil_div(a.seq, n), kChunk) * kChunk;
   if (n > 1 && steps < 32) steps = 32;
   p.parts = (int)ceil_div(a.seq, steps);
