@@ -302,6 +302,8 @@ struct SumOuts {
 };
 
 // 32 neighbouring values a block, by G warps that take every G-th part, eight loads at a time.
+// Eight warps, or 32 where there are few values or many parts for each: 74 parts of 24576
+// values take 6 us with eight and 15 with 32.
 template <int G>
 __global__ void __launch_bounds__(32 * G)
     sum_parts_kernel(const float* part, int64_t parts, int64_t n, SumOuts o) {
