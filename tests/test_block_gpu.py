@@ -329,6 +329,51 @@ def test_scan_extreme_decays(A):
         assert fits.all() or (k == "ddelta" and A < -1e37)
 
 
+@pytest.mark.parametrize("small", [False, True])
+def test_scan_growth_beyond_fp32_over_a_part(small):
+    """Growing states: one row's time is divided in parts, and e^128 over 32 steps is beyond fp32
+    though what it multiplies, 0 (small: 1e-30), leaves the state in range."""
+    T, D, N = 128, 8, 4
+    i = Inputs(9, False)
+    u, B, C, dout = i.normal(1, T, D), i.normal(1, T, 1, N), i.normal(1, T, 1, N), i.normal(1, T, D)
+    a, dl = torch.full((1, D, N), 4.0, device="cuda"), torch.ones(1, T, D, device="cuda")
+    # T * (a step's operations, and |d A| = 4 in units of the exponent's error) as above
+    ops = T * (8 + 8 * 4) + 64
+
+    def forward(u, dl, st):
+        out, so = torch.empty_like(u), torch.empty(1, D, N, device="cuda")
+        kept = torch.empty(zo.zo_scan_checkpoint_shape(u.shape, N), device="cuda")
+        zo.zo_scan(u, dl, a, B, C, out, softplus=False, state_in=st, state_out=so, checkpoints=kept)
+        args = (u, dl, a, B, C, None, None, None, False, None, st)
+        (want, last, _, _), (size, slast, _, _) = ref.scan(*args), ref.scan(*args, size=True)
+        near(out, want, size, ops, "out")
+        near(so, last, slast, ops, "state")
+        return kept
+
+    v, d = u.clone(), dl.clone()
+    if small:
+        v[:], d[:, 32:] = 0, 0
+        forward(v, d, 1e-30 * i.normal(1, D, N))
+    else:
+        v[:, :-8] = 0
+        forward(v, d, None)
+
+    v, d, ds = u.clone(), dl.clone(), None
+    if small:
+        v[:, -32:], d[:, :-32], ds = 0, 0, 1e-30 * i.normal(1, D, N)
+        dout[:] = 0
+    else:
+        v[:], dout[:, 8:] = 0, 0
+    kept = forward(v, d, None)
+    g = {k: torch.empty_like(t) for k, t in {"du": v, "ddelta": d, "dA": a, "dB": B, "dC": C}.items()}
+    zo.zo_scan_backward(v, d, a, B, C, dout, kept, g["du"], g["ddelta"], g["dA"], g["dB"], g["dC"],
+                        softplus=False, dstate_out=ds)
+    args = (v, d, a, B, C, dout, None, None, None, False, None, None, ds)
+    want, size = ref.scan_backward(*args), ref.scan_backward(*args, size=True)
+    for k in g:
+        near(g[k], want[k], size[k], 2 * ops + T, k)
+
+
 def test_scan_gradient_against_differences():
     """The kernel's gradients against central differences of the kernel's own forward."""
     R, T, D, N = 2, 12, 8, 4

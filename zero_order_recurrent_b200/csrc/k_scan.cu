@@ -438,6 +438,14 @@ __global__ void __launch_bounds__(128, 4)
 
 constexpr int kJoin = 8;  // parts whose results are loaded together
 
+// local + 2^x h: the state behind a part whose decays are 2^x together, as its steps would leave
+// it one after the other: a large growth of a small state stays finite, and that of the state 0
+// is 0.
+__device__ __forceinline__ float carried(float x, float h, float local) {
+  const float half = exp2_1(0.5f * x);
+  return h == 0.f ? local : fmaf(half * h, half, local);
+}
+
 // state[row][k] becomes the state that part k starts from.
 __global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims d, Parts parts) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, DN = (int64_t)d.D * d.N;
@@ -459,7 +467,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims
     for (int j = 0; j < kJoin; ++j)
       if (k0 + j < parts.n) {
         state[(k0 + j) * DN] = h;
-        h = fmaf(exp2_1(s[j] * A2), h, l[j]);
+        h = carried(s[j] * A2, h, l[j]);
       }
   }
 }
@@ -710,7 +718,7 @@ __global__ void __launch_bounds__(256) carry_join_kernel(zo_scan_args a, zo_scan
     for (int j = 0; j < kJoin; ++j)
       if (k0 - j >= 0) {
         state[(k0 - j) * DN] = v;
-        v = fmaf(exp2_1(s[j] * A2), v, l[j]);
+        v = carried(s[j] * A2, v, l[j]);
       }
   }
 }
