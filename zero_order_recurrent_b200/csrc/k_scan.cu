@@ -226,7 +226,7 @@ struct BC {
 // on from part to part, and then all parts run from the states they start with.
 // That takes the exponentials twice.
 //
-// Measured: 4096 rows x 10 steps x 1024 channels with states in and out 343 us (2.6 TB/s; by
+// Measured: 4096 rows x 10 steps x 1024 channels with states in and out 334 us (2.6 TB/s; by
 // the unit's count 196); 1 row x 16384 steps x 2048 channels in 37 parts 397 us (by its count
 // 276, the unit 60 to 70% busy).
 //
