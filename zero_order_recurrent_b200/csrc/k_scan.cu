@@ -2,9 +2,9 @@
 // y_t = sum_n C_t h_t + skip u_t, out_t = y_t silu(z_t), d_t = softplus(delta_t + bias);
 // its gradients; and its single-token form.  States, carries and sums are fp32.
 //
-// exp(d A) is 2^(d A log2(e)) by the special function unit (2^-22 relative).  It is not the
-// tensor cores' work: every channel and state has its own decay at every step, so no step is
-// a matrix product.  Times below are at 16 states and bf16.
+// exp(d A) is 2^(d A log2(e)) by the special function unit (2^-22 relative) and, near 1 where such
+// errors add up over a state's memory, a polynomial (decay_2).  It is not the tensor cores' work:
+// every channel and state has its own decay at every step, so no step is a matrix product.  Times below are at 16 states and bf16.
 #include <float.h>
 
 #include <initializer_list>
@@ -37,18 +37,32 @@ __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t ro
   return n < 0 ? 0 : T;
 }
 
-// 2^x, more exactly for |x| < 1/16.  The special function unit's results there are too small by
-// 6e-8 of themselves on average (measured: they are cut off rather than rounded), which over the
-// 1 / |x| steps that such a decay lasts adds up to 1e-6 of a state; so there a polynomial of
-// degree 3 that is 1 at 0 and has the least largest relative error up to 1/16 (2.7e-8; its
-// coefficients are the solution of that linear programme).  The backward pass uses it for the
-// carries, which halves the error of dA.
+// 2^x, near 1 to fp32's own precision.  The special function unit's results there (for x < 0) are
+// too small on average: by 5e-9 of themselves up to |x| = 2^-10, by 2.4e-8 from 2^-8 to 2^-5.  A decay
+// of 2^x lasts 1 / |x| steps and so adds 4e-6 to a state's relative error at |x| = 2^-8, 1.5e-5 at
+// 2^-12 (measured with varied steps; CUDA's expf: 7e-7 and 4e-5; a correctly rounded 2^x: 3e-7 and
+// 1e-6).  So up to 1/8 a polynomial of degree 4 that is 1 at 0 and has the least largest relative
+// error (3.1e-9; its coefficients are the solution of that linear programme): 3.4e-7 and 1.1e-6.
 __device__ __forceinline__ float2 exp2_slow_2(float2 x) {
   const float2 e = exp2_2(x);
-  float2 p = __ffma2_rn(x, two(0.0554962232708931f), two(0.2402576357126236f));
-  p = __ffma2_rn(x, p, two(0.6931472420692444f));
+  float2 p = __ffma2_rn(x, two(0.009628420695662498f), two(0.05553207919001579f));
+  p = __ffma2_rn(x, p, two(0.24022643268108368f));
+  p = __ffma2_rn(x, p, two(0.6931470632553101f));
   p = __ffma2_rn(x, p, two(1.f));
-  return make_float2(fabsf(x.x) < 0.0625f ? p.x : e.x, fabsf(x.y) < 0.0625f ? p.y : e.y);
+  return make_float2(fabsf(x.x) < 0.125f ? p.x : e.x, fabsf(x.y) < 0.125f ? p.y : e.y);
+}
+
+// The decay of a step, 2^(d A2).  With fp32 activations as above, which takes a sixth of the forward
+// pass's time.  With narrower ones, whose d, u and B are already rounded to 2^-9 or 2^-12, the unit's
+// own result with its argument moved by 8e-9, which costs nothing (decays of 1 stay 1): up to
+// |x| = 2^-10 it is then right on average (a state's error at 2^-12 falls from 1.5e-5 to 1.6e-6),
+// from 2^-8 on still 1.8e-8 too small (3e-6 at 2^-8).
+template <class T>
+__device__ __forceinline__ float2 decay_2(float2 d, float2 A2) {
+  if constexpr (sizeof(T) == 4)
+    return exp2_slow_2(__fmul2_rn(d, A2));
+  else
+    return exp2_2(__ffma2_rn(d, A2, two(8e-9f)));
 }
 
 // A log2(e), kept finite: the lowest fp32 as a decay rate gives decays of 0 and, at steps of
@@ -381,8 +395,8 @@ __global__ void __launch_bounds__(128, 4)
 #pragma unroll
               for (int i = 0; i < H; i += 2) {
                 const float4 b = B[i / 2];
-                h[i] = __ffma2_rn(exp2_2(__fmul2_rn(d1, A2[i])), h[i], __fmul2_rn(x1, make_float2(b.x, b.y)));
-                h[i + 1] = __ffma2_rn(exp2_2(__fmul2_rn(d1, A2[i + 1])), h[i + 1], __fmul2_rn(x1, make_float2(b.z, b.w)));
+                h[i] = __ffma2_rn(decay_2<T>(d1, A2[i]), h[i], __fmul2_rn(x1, make_float2(b.x, b.y)));
+                h[i + 1] = __ffma2_rn(decay_2<T>(d1, A2[i + 1]), h[i + 1], __fmul2_rn(x1, make_float2(b.z, b.w)));
                 if (!LOCAL) {
                   const float4 v = C[i / 2];
                   y = __ffma2_rn(make_float2(v.x, v.y), h[i], y);
@@ -442,7 +456,7 @@ constexpr int kJoin = 8;  // parts whose results are loaded together
 // it one after the other: a large growth of a small state stays finite, and that of the state 0
 // is 0.
 __device__ __forceinline__ float carried(float x, float h, float local) {
-  const float half = exp2_1(0.5f * x);
+  const float half = exp2_slow_2(two(0.5f * x)).x;
   return h == 0.f ? local : fmaf(half * h, half, local);
 }
 
@@ -537,7 +551,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, Sca
       float f[4];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const float2 v = __ffma2_rn(exp2_2(__fmul2_rn(d2, A2[p])), make_float2(h[k].v[2 * p], h[k].v[2 * p + 1]),
+        const float2 v = __ffma2_rn(decay_2<T>(d2, A2[p]), make_float2(h[k].v[2 * p], h[k].v[2 * p + 1]),
                                     __fmul2_rn(x, make_float2(to_f(B[k].v[2 * p]), to_f(B[k].v[2 * p + 1]))));
         y = __ffma2_rn(make_float2(to_f(C[k].v[2 * p]), to_f(C[k].v[2 * p + 1])), v, y);
         f[2 * p] = v.x, f[2 * p + 1] = v.y;
@@ -684,8 +698,8 @@ __global__ void __launch_bounds__(128, 4)
 #pragma unroll
         for (int i = 0; i < H; i += 2) {
           const float4 f = cs[i / 2];
-          v[i] = __fmul2_rn(exp2_2(__fmul2_rn(d1, A2[i])), __ffma2_rn(y1, make_float2(f.x, f.y), v[i]));
-          v[i + 1] = __fmul2_rn(exp2_2(__fmul2_rn(d1, A2[i + 1])), __ffma2_rn(y1, make_float2(f.z, f.w), v[i + 1]));
+          v[i] = __fmul2_rn(decay_2<T>(d1, A2[i]), __ffma2_rn(y1, make_float2(f.x, f.y), v[i]));
+          v[i + 1] = __fmul2_rn(decay_2<T>(d1, A2[i + 1]), __ffma2_rn(y1, make_float2(f.z, f.w), v[i + 1]));
         }
       }
     }
