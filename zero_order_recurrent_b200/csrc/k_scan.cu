@@ -52,9 +52,9 @@ __device__ __forceinline__ float2 exp2_slow_2(float2 x) {
   return make_float2(fabsf(x.x) < 0.125f ? p.x : e.x, fabsf(x.y) < 0.125f ? p.y : e.y);
 }
 
-// The decay of a step, 2^(d A2).  With fp32 activations as above, which takes a sixth of the forward
-// pass's time.  With narrower ones, whose d, u and B are already rounded to 2^-9 or 2^-12, the unit's
-// own result with its argument moved by 8e-9, which costs nothing (decays of 1 stay 1): up to
+// The decay of a step, 2^(d A2).  With fp32 activations as above, which takes a fifth of the forward
+// pass's time (1 row x 16384 steps x 2048 channels 401 and 494 us).  With narrower ones, whose d, u and
+// B are already rounded to 2^-9 or 2^-12, the unit's own result with its argument moved by 8e-9, which costs nothing (decays of 1 stay 1): up to
 // |x| = 2^-10 it is then right on average (a state's error at 2^-12 falls from 1.5e-5 to 1.6e-6),
 // from 2^-8 on still 1.8e-8 too small (3e-6 at 2^-8).
 template <class T>
@@ -245,9 +245,13 @@ struct BC {
 // 276, the unit 60 to 70% busy).
 //
 // A block takes `rows` rows of one set one after the other.
+//
+// GUARD: there are lanes with states beyond N, or there is no skip.  Those states are 0, as B is there,
+// and so is that skip, but 0 times an infinite d u or u is NaN: such a step puts the states back and
+// takes its y again, and adds no skip.  It takes 2 to 3% of the time.
 constexpr int kAhead = 4;
 
-template <class T, int S, int LN, bool LOCAL>
+template <class T, int S, int LN, bool LOCAL, bool GUARD>
 __global__ void __launch_bounds__(128, 4)
     scan_kernel(zo_scan_args a, ScanDims d, Parts parts, int rows, int copy_bc, bool wide) {
   constexpr int NP = S * LN, W = 32 / LN, H = S / 2;
@@ -403,11 +407,21 @@ __global__ void __launch_bounds__(128, 4)
                   y = __ffma2_rn(make_float2(v.z, v.w), h[i + 1], y);
                 }
               }
+              if (GUARD && !(fabsf(x1.x) <= FLT_MAX)) {
+                y = two(0.f);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                  if (n0 + 2 * i >= d.N) h[i].x = 0.f;
+                  if (n0 + 2 * i + 1 >= d.N) h[i].y = 0.f;
+                  y = __ffma2_rn(reinterpret_cast<const float2*>(C)[i], h[i], y);
+                }
+              }
               if (!LOCAL) {
                 float v = y.x + y.y;
 #pragma unroll
                 for (int m = W; m < 32; m *= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
-                v = fmaf(skip, e ? u.y : u.x, v) * (e ? gz.y : gz.x);
+                if (!GUARD || a.skip.ptr) v = fmaf(skip, e ? u.y : u.x, v);
+                v *= e ? gz.y : gz.x;
                 if (on && q == 0) out[(j + e) * a.out.step] = from_f<T>(v);
               }
             }
@@ -489,8 +503,9 @@ __global__ void __launch_bounds__(256) scan_join_kernel(zo_scan_args a, ScanDims
 // One token.  A thread holds four states of a channel and walks RG rows of a
 // set, so that A is read once for them; all its loads are issued before the first result is
 // waited for.  Bound: the states, read and written: 512 rows x 4096 channels take 60 us, 4.8 TB/s.
-// HOW: 2 - every lane has four states, which, like those of A, B and C, are on 16 (8) bytes;
-// 1 - so, but lanes behind the last state have none; 0 - states one at a time.
+// HOW: 2 - there is a skip, and every lane has four states, which, like those of A, B and C, are on
+// 16 (8) bytes; 3 - so, without skip; 1 - so, but lanes behind the last state may have none;
+// 0 - states one at a time.
 template <class T, int LN, int RG, int HOW>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, ScanDims d, unsigned groups) {
   const unsigned nb = ((unsigned)d.D * LN + kThreads - 1) / kThreads;  // blocks of a row
@@ -504,7 +519,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, Sca
   const int64_t g = c / d.Dg, cn = (int64_t)c * d.N;
   auto four = [&](auto* p, auto& x) {  // p[n0 ..], zeros from N on
     using E = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
-    if constexpr (HOW == 2) {
+    if constexpr (HOW >= 2) {
       x = *reinterpret_cast<const Vec<E, 4>*>(p + n0);
     } else if constexpr (HOW == 1) {
       x = load_if<E, 4>(p + n0, n0 < d.N);
@@ -553,13 +568,19 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, Sca
       for (int p = 0; p < 2; ++p) {
         const float2 v = __ffma2_rn(decay_2<T>(d2, A2[p]), make_float2(h[k].v[2 * p], h[k].v[2 * p + 1]),
                                     __fmul2_rn(x, make_float2(to_f(B[k].v[2 * p]), to_f(B[k].v[2 * p + 1]))));
-        y = __ffma2_rn(make_float2(to_f(C[k].v[2 * p]), to_f(C[k].v[2 * p + 1])), v, y);
+        float2 in_y = v;  // states beyond N (of lanes, or one by one) add nothing, not even where d u is infinite
+        if (HOW == 0 && n0 + 2 * p >= d.N) in_y.x = 0.f;
+        if (HOW == 0 && n0 + 2 * p + 1 >= d.N) in_y.y = 0.f;
+        if (HOW == 1 && n0 >= d.N) in_y = two(0.f);
+        y = __ffma2_rn(make_float2(to_f(C[k].v[2 * p]), to_f(C[k].v[2 * p + 1])), in_y, y);
         f[2 * p] = v.x, f[2 * p + 1] = v.y;
       }
       const int64_t row = r0 + k;
       if (on && a.state_out.ptr)
         store_states4<HOW != 0>(a.state_out.ptr + row * a.state_out.stride + cn, n0, d.N, f);
-      const float out = fmaf(skip, e ? uu.y : uu.x, sum_lanes<LN>(y.x + y.y)) * (e ? gate.y : gate.x);
+      float out = sum_lanes<LN>(y.x + y.y);
+      if (HOW == 2 || (HOW < 2 && a.skip.ptr)) out = fmaf(skip, e ? uu.y : uu.x, out);
+      out *= e ? gate.y : gate.x;
       if (on && q == 0) static_cast<T*>(a.out.ptr)[row * a.out.row + c] = from_f<T>(out);
     }
   }
@@ -745,12 +766,13 @@ constexpr int kFlush = 64;   // chunks after which the parameters' sums are put 
 template <int LN>
 constexpr int kBackWarps = LN >= 4 ? 4 : LN;
 
-template <int LN, int WARPS>
+template <int LN, int WARPS, int ZEROS>
 struct BackTile {
   static constexpr int kWarps = WARPS, kThreads = 32 * kWarps;
   static constexpr int kWarpChannels = 128 / LN, kChannels = kWarps * kWarpChannels;
   static constexpr int NP = 4 * LN, kMid = kChunk / kBlock - 1;
-  alignas(16) float d[kChunk][kChannels], u[kChunk][kChannels], dy[kChunk][kChannels];
+  static constexpr int kRows = kChunk + ZEROS;             // ZEROS: a row of zeros behind the steps
+  alignas(16) float d[kRows][kChannels], u[kRows][kChannels], dy[kRows][kChannels];
   float slope[kChunk][kChannels], zf[kChunk][kChannels];   // softplus'(raw), dout silu'(z)
   alignas(16) float2 B[kChunk][NP], C[kChunk][NP];         // each twice, for pairs of channels
   alignas(16) float4 mid[kMid][4][kThreads];               // the states before the later blocks
@@ -782,10 +804,15 @@ struct BackSums {
 // carries, against 42 us of memory traffic for the whole training step.  Blocks of one warp
 // serve narrow groups: 12 rows x 2288 steps x 40 channels in 4 groups, forward and backward,
 // 581 us with blocks of four warps only and 335 with either.
-template <class T, int LN, int WARPS>
+//
+// GUARD: there are states beyond N (1 - whole lanes of them, if any; 2 - parts of lanes too), or there
+// is no skip.  Those states and their carries and that skip are 0, but 0 times an infinite d u or dy is
+// NaN.  So such lanes read zeros for these, and single states are left out of all sums.  It takes 1 to
+// 2% of the time, 4% at 12 states and 7% at 3.
+template <class T, int LN, int WARPS, int GUARD>
 __global__ void __launch_bounds__(32 * WARPS, LN >= 4 ? 12 / WARPS : 6 / WARPS)
     scan_backward_kernel(zo_scan_args a, zo_scan_grads g, ScanDims d, Parts parts, BackSums sums, bool vec) {
-  using S = BackTile<LN, WARPS>;
+  using S = BackTile<LN, WARPS, GUARD != 0>;
   extern __shared__ __align__(16) unsigned char smem[];
   S& sh = *reinterpret_cast<S*>(smem);
   const unsigned tiles = d.tiles * d.G;
@@ -901,6 +928,9 @@ __global__ void __launch_bounds__(32 * WARPS, LN >= 4 ? 12 / WARPS : 6 / WARPS)
   for (int e = 0; e < 4; ++e)
     bias[e] = a.delta_bias.ptr && pc + e < left ? a.delta_bias.ptr[set * a.delta_bias.stride + c0 + pc + e] : 0.f;
 
+  const bool none = GUARD && LN > 2 && n0 >= d.N;  // a lane without states
+  if (GUARD)
+    for (int i = tid; i < S::kChannels; i += S::kThreads) sh.d[S::kRows - 1][i] = sh.u[S::kRows - 1][i] = sh.dy[S::kRows - 1][i] = 0.f;
   int chunks = 0;
   for (int t0 = end > tb ? tb + (end - 1 - tb) / kChunk * kChunk : tb - 1; t0 >= tb; t0 -= kChunk) {
     __syncthreads();
@@ -982,8 +1012,9 @@ __global__ void __launch_bounds__(32 * WARPS, LN >= 4 ? 12 / WARPS : 6 / WARPS)
       f[2] = make_float2(y.x, y.y), f[3] = make_float2(y.z, y.w);
     };
     auto step = [&](auto slow, int s, float2 (&h)[4][2], float2 (&at)[4][2]) {
-      const float4 dt = *reinterpret_cast<const float4*>(&sh.d[s][ch]);
-      const float4 u = *reinterpret_cast<const float4*>(&sh.u[s][ch]);
+      const int at_s = none ? S::kRows - 1 : s;
+      const float4 dt = *reinterpret_cast<const float4*>(&sh.d[at_s][ch]);
+      const float4 u = *reinterpret_cast<const float4*>(&sh.u[at_s][ch]);
       float2 b[4];
       load4(&sh.B[s][n0], b);
       const float2 d2[2] = {make_float2(dt.x, dt.y), make_float2(dt.z, dt.w)};
@@ -1037,9 +1068,10 @@ __global__ void __launch_bounds__(32 * WARPS, LN >= 4 ? 12 / WARPS : 6 / WARPS)
 #pragma unroll
       for (int j = kSub - 1; j >= 0; --j) {
         const int s = m * kSub + j;
-        const float4 d4 = *reinterpret_cast<const float4*>(&sh.d[s][ch]);
-        const float4 u4 = *reinterpret_cast<const float4*>(&sh.u[s][ch]);
-        const float4 y4 = *reinterpret_cast<const float4*>(&sh.dy[s][ch]);
+        const int at_s = none ? S::kRows - 1 : s;
+        const float4 d4 = *reinterpret_cast<const float4*>(&sh.d[at_s][ch]);
+        const float4 u4 = *reinterpret_cast<const float4*>(&sh.u[at_s][ch]);
+        const float4 y4 = *reinterpret_cast<const float4*>(&sh.dy[at_s][ch]);
         float2 b[4], c[4];
         load4(&sh.B[s][n0], b);
         load4(&sh.C[s][n0], c);
@@ -1058,11 +1090,12 @@ __global__ void __launch_bounds__(32 * WARPS, LN >= 4 ? 12 / WARPS : 6 / WARPS)
           v[4 + n] = tc2.x + tc2.y;
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            y[p] = __ffma2_rn(c[n], hs[j + 1][n][p], y[p]);
-            gB[p] = __ffma2_rn(b[n], gr[n][p], gB[p]);
+            const bool real = GUARD < 2 || n0 + n < d.N;
+            if (real) y[p] = __ffma2_rn(c[n], hs[j + 1][n][p], y[p]);
+            if (real) gB[p] = __ffma2_rn(b[n], gr[n][p], gB[p]);
             gr[n][p] = __fmul2_rn(gr[n][p], at[j][n][p]);
             const float2 w = __fmul2_rn(gr[n][p], hs[j][n][p]);
-            gA[p] = __ffma2_rn(w, A2[n][p], gA[p]);
+            if (real) gA[p] = __ffma2_rn(w, A2[n][p], gA[p]);
             dA[n][p] = __ffma2_rn(w, d2[p], dA[n][p]);
           }
         }
@@ -1101,9 +1134,10 @@ __global__ void __launch_bounds__(32 * WARPS, LN >= 4 ? 12 / WARPS : 6 / WARPS)
             cs[i] = fmaf(dyk, u, cs[i]);
             cb[i] += dr;
             if (k < left) {
-              wu[i] = from_f<T>(fmaf(r[3 * i + 1], sh.d[s][k], skip[i] * dyk));
+              const bool skips = !GUARD || a.skip.ptr;
+              wu[i] = from_f<T>(fmaf(r[3 * i + 1], sh.d[s][k], skips ? skip[i] * dyk : 0.f));
               wd[i] = from_f<T>(dr);
-              if (gate) wz[i] = from_f<T>(sh.zf[s][k] * fmaf(skip[i], u, r[3 * i + 2]));
+              if (gate) wz[i] = from_f<T>(sh.zf[s][k] * (skips ? fmaf(skip[i], u, r[3 * i + 2]) : r[3 * i + 2]));
             }
           }
       }
@@ -1233,8 +1267,8 @@ cudaError_t run_scan(const zo_scan_args& a, float* ws, cudaStream_t st) {
   constexpr int kSmem = (int)sizeof(BC<T, S * LN>);
   cudaError_t e = cudaSuccess;
   if (plan.parts > 1) {
-    if ((e = allow_shared(scan_kernel<T, S, LN, true>, kSmem)) != cudaSuccess) return e;
-    scan_kernel<T, S, LN, true><<<(unsigned)(per_row * row_blocks * (plan.parts - 1)), threads, kSmem, st>>>(
+    if ((e = allow_shared(scan_kernel<T, S, LN, true, false>, kSmem)) != cudaSuccess) return e;
+    scan_kernel<T, S, LN, true, false><<<(unsigned)(per_row * row_blocks * (plan.parts - 1)), threads, kSmem, st>>>(
         a, d, parts, (int)rows, copy, d.N % 4 == 0);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -1242,8 +1276,9 @@ cudaError_t run_scan(const zo_scan_args& a, float* ws, cudaStream_t st) {
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = allow_shared(scan_kernel<T, S, LN, false>, kSmem)) != cudaSuccess) return e;
-  scan_kernel<T, S, LN, false><<<(unsigned)blocks, threads, kSmem, st>>>(a, d, parts, (int)rows, copy, wide);
+  auto kernel = d.N < S * LN || !a.skip.ptr ? scan_kernel<T, S, LN, false, true> : scan_kernel<T, S, LN, false, false>;
+  if ((e = allow_shared(kernel, kSmem)) != cudaSuccess) return e;
+  kernel<<<(unsigned)blocks, threads, kSmem, st>>>(a, d, parts, (int)rows, copy, wide);
   count_launch();
   return cudaGetLastError();
 }
@@ -1259,8 +1294,10 @@ cudaError_t run_scan_step(const zo_scan_args& a, cudaStream_t st) {
   for (const zo_f32* p : {&a.A, &a.state_in, &a.state_out})
     wide = wide && p->stride % 4 == 0 && reinterpret_cast<uintptr_t>(p->ptr) % 16 == 0;
   for (const zo_tensor* t : {&a.B, &a.C}) wide = wide && vec_width(*t, sizeof(T), 4, 4) == 4;
-  if (wide && d.N == 4 * LN)
+  if (wide && d.N == 4 * LN && a.skip.ptr)
     scan_step_kernel<T, LN, RG, 2><<<(unsigned)blocks, kThreads, 0, st>>>(a, d, (unsigned)groups);
+  else if (wide && d.N == 4 * LN)
+    scan_step_kernel<T, LN, RG, 3><<<(unsigned)blocks, kThreads, 0, st>>>(a, d, (unsigned)groups);
   else if (wide)
     scan_step_kernel<T, LN, RG, 1><<<(unsigned)blocks, kThreads, 0, st>>>(a, d, (unsigned)groups);
   else
@@ -1332,10 +1369,14 @@ cudaError_t run_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, flo
   for (const zo_tensor* t : {&a.u, &a.delta, &a.z, &g.dout})
     vec = vec && vec_width(*t, sizeof(T), d.Dg, 4) == 4;
   auto launch = [&](auto warps) {
-    constexpr int W = decltype(warps)::value, kSmem = (int)sizeof(BackTile<LN, W>);
-    const cudaError_t r = allow_shared(scan_backward_kernel<T, LN, W>, kSmem);
+    constexpr int W = decltype(warps)::value;
+    const int guard = d.N % 4 ? 2 : d.N < 4 * LN || !a.skip.ptr ? 1 : 0;
+    const int smem = guard ? (int)sizeof(BackTile<LN, W, 1>) : (int)sizeof(BackTile<LN, W, 0>);
+    auto kernel = guard == 2 ? scan_backward_kernel<T, LN, W, 2>
+                  : guard ? scan_backward_kernel<T, LN, W, 1> : scan_backward_kernel<T, LN, W, 0>;
+    const cudaError_t r = allow_shared(kernel, smem);
     if (r != cudaSuccess) return r;
-    scan_backward_kernel<T, LN, W><<<(unsigned)blocks, 32 * W, kSmem, st>>>(a, g, d, parts, sums, vec);
+    kernel<<<(unsigned)blocks, 32 * W, smem, st>>>(a, g, d, parts, sums, vec);
     count_launch();
     return cudaGetLastError();
   };
