@@ -231,6 +231,12 @@ class _Call:
             self.fail(name, f"must be contiguous of shape {(n,)}")
         return t.data_ptr()
 
+    def pack(self, structure, values):
+        try:
+            return _PACK[structure](*values)
+        except (struct.error, OverflowError, TypeError) as e:
+            raise ValueError(f"{self.where}: a size or eps does not fit the call ({e})") from None
+
     def run(self, name, *args, stream=None, workspace=None):
         """Calls `name` on the tensors' device.  workspace: None for a call without
         one, else (the caller's tensor or None, bytes)."""
@@ -300,11 +306,12 @@ def _conv_args(c, x, weight, out, bias, silu, lengths, state_in, state_out, stat
     # a window of one tap holds nothing
     st = [_NONE3 if K == 1 else c.act(n, t, win, dt, True)
           for n, t in (("state_in", state_in), ("state_out", state_out))]
-    return (K, S), _PACK[ConvArgs](
+    args = (
         R, T, D, K, S, c.code(x), ZO_CONV_SILU if silu else 0, *c.act("x", x, x.shape, dt),
         *c.act("out", out, x.shape, dt, True), *c.param("weight", weight, (K, D), S),
         *c.param("bias", bias, (D,), S, True), c.ints("lengths", lengths, R), *st[0], *st[1],
         c.ints("status", status, 1))
+    return (K, S), c.pack(ConvArgs, args)
 
 
 def zo_conv(x, weight, out, bias=None, silu=True, lengths=None, state_in=None, state_out=None,
@@ -377,7 +384,7 @@ def _scan_args(c, u, delta, A, B, C, out, skip, z, delta_bias, softplus, lengths
                 not checkpoints.is_contiguous():
             c.fail("checkpoints", "must be contiguous of zo_scan_checkpoint_shape()")
         kept = checkpoints.data_ptr()
-    return (N, S), _PACK[ScanArgs](
+    args = (
         R, T, D, G, N, S, c.code(u), ZO_SCAN_SOFTPLUS if softplus else 0,
         *c.act("u", u, u.shape, dt), *c.act("delta", delta, u.shape, dt),
         *c.act("out", out, u.shape, dt, True), *c.act("z", z, u.shape, dt, True),
@@ -386,6 +393,7 @@ def _scan_args(c, u, delta, A, B, C, out, skip, z, delta_bias, softplus, lengths
         *c.param("delta_bias", delta_bias, (D,), S, True), c.ints("lengths", lengths, R),
         *c.states("state_in", state_in, (R, D, N)), *c.states("state_out", state_out, (R, D, N)),
         kept, c.ints("status", status, 1))
+    return (N, S), c.pack(ScanArgs, args)
 
 
 def zo_scan(u, delta, A, B, C, out, skip=None, z=None, delta_bias=None, softplus=True,
@@ -452,13 +460,14 @@ def _norm_args(c, x, x_out, n_out, o, gate, w_post, scale, w_pre, eps, gate_firs
     dt = like.dtype if like is not None else x.dtype
     R, D = x.shape
     S = _sets((w_post, 1), (scale, 1), (w_pre, 1))
-    return S, _PACK[NormArgs](
+    args = (
         R, D, S, c.code(like if like is not None else x), c.code(x),
         ZO_NORM_GATE_FIRST if gate_first else 0, eps, *c.act("x", x, x.shape, x.dtype),
         *c.act("x_out", x_out, x.shape, x.dtype, True), *c.act("o", o, x.shape, dt, True),
         *c.act("gate", gate, x.shape, dt, True), *c.act("n_out", n_out, x.shape, dt, True),
         *c.param("w_post", w_post, (D,), S, True), *c.param("scale", scale, (D,), S, True),
         *c.param("w_pre", w_pre, (D,), S, True))
+    return S, c.pack(NormArgs, args)
 
 
 def zo_block_norm(x, x_out=None, n_out=None, o=None, gate=None, w_post=None, scale=None,
