@@ -8,8 +8,8 @@
 // pairs of channels for the packed fp32 instructions, so x is read once per run plus
 // K - 1 steps of overlap; the next U steps are on their way while U are computed.
 // Measured at 8 rows x 2048 steps x 4096 channels, K = 4, bf16: forward 68 us (4.0 TB/s),
-// backward 167 us (2.4 TB/s).  Neither wider accesses nor more steps ahead nor more
-// blocks an SM change the forward by more than a tenth.
+// backward 168 us (2.4 TB/s).  Both wait for loads, with no pipe above 55%.  Neither wider
+// accesses nor more steps ahead nor more blocks an SM change the forward by more than a tenth.
 #include <initializer_list>
 #include <type_traits>
 
@@ -22,7 +22,11 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// Blocks of an SM that the registers allow.
+// Blocks of an SM that the registers allow.  At the sizes above, in us by blocks an SM; forward:
+// 4 taps 70 with 7, 72 with 6, 74 with 5; 6 taps 118, 83 and 84; 8 taps 97 with 5, 98 with 4, 113
+// with 3.  Backward: 2, 3 and 4 taps 131, 150 and 168 with 4, 153, 166 and 177 with 3 (fp32 4 taps
+// 177 and 151, channels one by one 211 and 147: they spill); 5 taps 191, 189 and 226 with 4, 3 and
+// 2; 6 taps 316, 212 and 249; 8 taps 709, 283 and 264.
 constexpr int held_forward(int taps) { return taps <= 4 ? 7 : taps <= 6 ? 5 : 4; }
 constexpr int held_backward(int taps) { return taps <= 4 ? 4 : taps <= 5 ? 3 : 2; }
 

@@ -383,7 +383,9 @@ __global__ void __launch_bounds__(block_of<W>(), V * E <= 8 ? 512 / block_of<W>(
     }
 }
 
-// Threads of a row in the backward pass.
+// Threads of a row in the backward pass.  Rows of more than 8192 channels take 1024 threads with 64
+// registers each, some of them spilled; with 512 threads and 32 channels a thread 2048 x 16384 takes
+// 580 instead of 845 us (but 8 x 16384 55 instead of 49; the forward 161 instead of 139).
 int backward_width(int channels) {
   return channels <= 256 ? 32 : channels <= 512 ? 64 : channels <= 1024 ? 128 : channels <= 2048 ? 256
          : channels <= 8192 ? 512 : 1024;

@@ -1,10 +1,11 @@
 // Selective scan: per row, channel and state h_t = exp(d_t A) h_{t-1} + d_t u_t B_t,
 // y_t = sum_n C_t h_t + skip u_t, out_t = y_t silu(z_t), d_t = softplus(delta_t + bias);
-// its gradients; and its single-token form.  States, carries and sums are fp32.
+// and its single-token form.  States, carries and sums are fp32.  (Gradients: k_scan_backward.cu.)
 //
 // exp(d A) is 2^(d A log2(e)) by the special function unit (2^-22 relative) and, near 1 where such
 // errors add up over a state's memory, a polynomial (decay_2).  It is not the tensor cores' work:
-// every channel and state has its own decay at every step, so no step is a matrix product.  Times below are at 16 states and bf16.
+// every channel and state has its own decay at every step, so no step is a matrix product.  Times
+// below are at 16 states and bf16.
 #include "k_scan.cuh"
 
 namespace zo {
@@ -23,7 +24,7 @@ struct BC {
 // u, delta and z come straight into registers kAhead steps ahead.
 //
 // Bound: the special function unit, 16 results a clock and SM.  A value with 16
-// states takes 16 exponentials and 5 for softplus and silu, so 21 / 16 clocks; its
+// states takes 16 exponentials and 4 for softplus and silu, so 20 / 16 clocks; its
 // 8 bytes in bf16 take 0.34 clocks of an SM's share of the memory.  The 16
 // exponentials of one step are independent.  Four states a lane and four warps along
 // time, each keeping its decays in registers for a second run, make more warps without parts,
@@ -32,11 +33,13 @@ struct BC {
 // Where rows and channels are too few for the SMs, time is divided as well: LOCAL
 // runs each part but the last from the state 0, scan_join_kernel passes the states
 // on from part to part, and then all parts run from the states they start with.
-// That takes the exponentials twice.
+// That takes the exponentials and softplus twice.
 //
-// Measured: 4096 rows x 10 steps x 1024 channels with states in and out 334 us (2.6 TB/s; by
-// the unit's count 196); 1 row x 16384 steps x 2048 channels in 37 parts 397 us (by its count
-// 276, the unit 60 to 70% busy).
+// Measured: 4096 rows x 10 steps x 1024 channels with states in and out 333 us (2.6 TB/s; by
+// the unit's count 186, which is 56% busy: the rest waits between dependent products, for a row's
+// state and at a tile's barriers, with 4 warps a scheduler); 1 row x 16384 steps x 2048 channels in
+// 37 parts 397 us (by its count 280, 77% busy from the state 0 and 70% with the states).  With fp32
+// activations 374 and 494 us.
 //
 // A block takes `rows` rows of one set one after the other.
 //
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(zo_scan_args a, Sca
 template <class T, int S, int LN>
 cudaError_t run_scan(const zo_scan_args& a, float* ws, cudaStream_t st) {
   const ScanPlan plan = scan_plan(a);
-  ScanDims d = scan_dims<LN>(a);
+  ScanDims d = scan_dims(a);
   d.tiles = plan.tiles;
   const int64_t DN = (int64_t)d.D * d.N;
   const Parts parts{plan.parts, plan.steps, ws, ws + (int64_t)a.rows * plan.parts * DN};
@@ -410,7 +413,7 @@ cudaError_t run_scan(const zo_scan_args& a, float* ws, cudaStream_t st) {
 
 template <class T, int LN, int RG>
 cudaError_t run_scan_step(const zo_scan_args& a, cudaStream_t st) {
-  const ScanDims d = scan_dims<LN>(a);
+  const ScanDims d = scan_dims(a);
   const int64_t groups = ceil_div(d.rows_per_set, RG) * RG;  // rows of a set, whole groups
   const int64_t blocks = ceil_div((int64_t)d.D * LN, kThreads) * (groups / RG) * a.sets;
   if (blocks > INT32_MAX || (int64_t)d.D * LN > INT32_MAX || groups * a.sets > UINT32_MAX)
@@ -452,7 +455,9 @@ cudaError_t launch_scan_step(const zo_scan_args& a, cudaStream_t st) {
       using T = decltype(t);
       constexpr int LN = decltype(ln)::value;
       // Several rows a thread once that leaves enough threads for the memory's latency: one and
-      // four rows a thread take 110 and 79 us for 512 rows of 4096 channels, the same for 64.
+      // four rows a thread take 93 and 62 us for 512 rows of 4096 channels in one set, 22 and 23 for
+      // 64.  A set's last thread loads its last row again for those that it lacks: in sets of four
+      // and five rows 95 and 68, 95 and 83, of two 97 either way, and of one row 99 and 161.
       const int64_t threads = (int64_t)a.rows * a.channels * LN;
       return threads >= 4ll * kBlockSMs * 2048 ? run_scan_step<T, LN, 4>(a, st)
                                                : run_scan_step<T, LN, 1>(a, st);

@@ -22,7 +22,7 @@ struct ScanDims {
   int64_t T;
   int D, N, G, Dg;        // channels, states, groups, channels of a group
   int rows_per_set;
-  int tiles;              // channel tiles of a group
+  int tiles = 0;          // channel tiles of a group
   int64_t chunks;
 };
 
@@ -52,9 +52,9 @@ __device__ __forceinline__ float2 exp2_slow_2(float2 x) {
 
 // The decay of a step, 2^(d A2).  With fp32 activations as above, which takes a fifth of the forward
 // pass's time (1 row x 16384 steps x 2048 channels 401 and 494 us).  With narrower ones, whose d, u and
-// B are already rounded to 2^-9 or 2^-12, the unit's own result with its argument moved by 8e-9, which costs nothing (decays of 1 stay 1): up to
-// |x| = 2^-10 it is then right on average (a state's error at 2^-12 falls from 1.5e-5 to 1.6e-6),
-// from 2^-8 on still 1.8e-8 too small (3e-6 at 2^-8).
+// B are already rounded to 2^-9 or 2^-12, the unit's own result with its argument moved by 8e-9, which
+// costs nothing (decays of 1 stay 1): up to |x| = 2^-10 it is then right on average (a state's error
+// at 2^-12 falls from 1.5e-5 to 1.6e-6), from 2^-8 on still 1.8e-8 too small (3e-6 at 2^-8).
 template <class T>
 __device__ __forceinline__ float2 decay_2(float2 d, float2 A2) {
   if constexpr (sizeof(T) == 4)
@@ -223,7 +223,6 @@ __device__ __forceinline__ float carried(float x, float h, float local) {
   return h == 0.f ? local : fmaf(half * h, half, local);
 }
 
-template <int LN>
 ScanDims scan_dims(const zo_scan_args& a) {
   ScanDims d;
   d.T = a.seq;
@@ -232,7 +231,6 @@ ScanDims scan_dims(const zo_scan_args& a) {
   d.G = a.groups;
   d.Dg = a.channels / a.groups;
   d.rows_per_set = a.rows / a.sets;
-  d.tiles = (int)ceil_div(d.Dg, kThreads / LN);
   d.chunks = ceil_div(a.seq, kChunk);
   return d;
 }
@@ -258,8 +256,8 @@ int lanes_per_channel(int N) {
 
 // Warps of a block (at most four, and no more than a group's channels fill),
 // and the parts of time.  A warp alone on its scheduler keeps the special function
-// unit busy a third of the time, and in parts the exponentials come twice (37 instead of
-// 21 results a value), so time is divided where there are under 4/3 warps for each of the 592
+// unit busy a third of the time, and in parts the exponentials come twice (38 instead of
+// 20 results a value), so time is divided where there are under 4/3 warps for each of the 592
 // schedulers, into as many parts as make four blocks an SM at most (which is what stays there),
 // of 32 steps at least.  2048 steps of 2048 channels in one pass and in parts: 2 rows (128
 // warps) 452 and 131 us, 4 rows 455 and 223, 8 rows 457 and 408, 12 rows 578 and 543.

@@ -216,10 +216,14 @@ struct BackSums {
 // keep every state in memory.  More steps in registers, or all states before kSub steps in
 // shared memory, leave two blocks an SM instead of three (576 against 561 us, 649 against 561).
 //
-// Bound: issue, at 570 instructions for 32 channels, 16 states and a step, half of the slots
-// used with three warps a scheduler; the multiply-add pipe and the special function unit (43 of its
-// results a value) follow.  4 rows x 2048 steps x 2048 channels: 561 us, and 124 us for the
-// carries, against 42 us of memory traffic for the whole training step.  Blocks of one warp
+// Bound: latency.  It takes 570 instructions for 32 channels, 16 states and a step and 42 results
+// of the special function unit a value, but no pipe is above 32% and 53% of the issue slots are used:
+// 2.4 warps a scheduler do not hide the waits between dependent products and for a chunk's inputs.
+// 4 rows x 2048 steps x 2048 channels: 562 us, and 124 us for the carries (their unit 67% busy),
+// against 42 us of memory traffic for the whole training step.  Up to 8 states six warps an SM stay,
+// at 254 registers a thread: with twelve and 168, and parts of time to match, 4 and 8 states take
+// 531 and 578 us instead of 612 and 618 for those rows, and 1058 and 817 instead of 841 and 762
+// for 32 x 512.  Blocks of one warp
 // serve narrow groups: 12 rows x 2288 steps x 40 channels in 4 groups, forward and backward,
 // 581 us with blocks of four warps only and 335 with either.
 //
@@ -636,7 +640,7 @@ template <class T, int LN, int S, int LC>
 cudaError_t run_scan_backward(const zo_scan_args& a, const zo_scan_grads& g, float* ws,
                               cudaStream_t st) {
   const BackPlan p = back_plan<LN>(a);
-  ScanDims d = scan_dims<LN>(a);
+  ScanDims d = scan_dims(a);
   d.tiles = p.tiles;
   const int64_t DN = (int64_t)d.D * d.N, blocks = (int64_t)p.tiles * d.G * a.rows * p.parts;
   const int64_t bc = (int64_t)a.rows * d.T * d.G * 2 * d.N;
