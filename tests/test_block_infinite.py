@@ -97,3 +97,35 @@ def test_infinite_inputs_and_gradients(N, T, dtype, skip):
         there = ~torch.isnan(want[k])
         assert torch.equal(torch.isnan(got), ~there), k
         same(got[there], want[k][there])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R", [1, 700])
+def test_infinities_outlast_decays_that_vanish_together(R, dtype):
+    """No step's decay is 0, but those of 32 steps together are below fp32: an infinite state, and an
+    infinite gradient, stay infinite over them, whether or not time is divided there."""
+    T, D, N = 140, 6, 8
+    u, _, z, dout, _, B, C = inputs(R, T, D, N, dtype)
+    dl, A = torch.full_like(u, 5.0), torch.full((D, N), -4.0, device="cuda")   # e^-20 a step
+    u[0, 3, 1] = INF
+    st, so = torch.ones(R, D, N, device="cuda"), torch.empty(R, D, N, device="cuda")
+    st[0, 4, 2] = INF
+    out, kept = torch.empty_like(u), torch.empty(zo.zo_scan_checkpoint_shape(u.shape, N), device="cuda")
+    zo.zo_scan(u, dl, A, B, C, out, z=z, softplus=False, state_in=st, state_out=so, checkpoints=kept)
+    want, last, _, _ = ref.scan(u, dl, A[None], B, C, z=z, softplus=False, state=st)
+    assert torch.isinf(want[0]).sum() == T - 3 + T and torch.isinf(last[0]).sum() == N + 1
+    same(out, want)
+    same(so, last)
+
+    u[0, 3, 1], st[0, 4, 2] = 1, 1
+    dso, dsi = torch.ones_like(st), torch.empty_like(st)
+    dso[0, 4, 2], dout[0, T - 2, 1] = INF, INF
+    zo.zo_scan(u, dl, A, B, C, out, z=z, softplus=False, state_in=st, checkpoints=kept)
+    du, dd, dz, dB, dC, dA = (torch.empty_like(t) for t in (u, dl, z, B, C, A))
+    zo.zo_scan_backward(u, dl, A, B, C, dout, kept, du, dd, dA, dB, dC, z=z, dz=dz, softplus=False, dstate_out=dso,
+                        dstate_in=dsi)
+    want = ref.scan_backward(u, dl, A[None], B, C, dout, z=z, softplus=False, state=st, dstate=dso)
+    assert torch.isinf(want["dstate_in"][0]).sum() == N + 1
+    want["du"][0, T - 2, 1] = INF  # (the reference has a skip of 0 there)
+    for got, k in ((du, "du"), (dB, "dB"), (dC, "dC"), (dz, "dz"), (dsi, "dstate_in"), (dA[None], "dA")):
+        same(got, want[k])

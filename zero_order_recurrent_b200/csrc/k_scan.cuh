@@ -216,11 +216,13 @@ constexpr int kAhead = 4;     // steps of a channel's inputs in registers ahead
 constexpr int kJoin = 8;  // parts whose results are loaded together
 
 // local + 2^x h: the state behind a part whose decays are 2^x together, as its steps would leave
-// it one after the other: a large growth of a small state stays finite, and that of the state 0
-// is 0.
+// it one after the other: a large growth of a small state stays finite, that of the state 0 is 0, and
+// an infinite state stays so though no fp32 is as small as its decays together.
 __device__ __forceinline__ float carried(float x, float h, float local) {
   const float half = exp2_slow_2(two(0.5f * x)).x;
-  return h == 0.f ? local : fmaf(half * h, half, local);
+  if (h == 0.f) return local;
+  if (fabsf(h) > FLT_MAX && x >= -FLT_MAX) return h + local;
+  return fmaf(half * h, half, local);
 }
 
 ScanDims scan_dims(const zo_scan_args& a) {
