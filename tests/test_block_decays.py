@@ -47,7 +47,7 @@ def bound(step, dtype):
     tol = U * (M ** 0.5 + 4)
     if dtype is not torch.float32:
         # the special function unit's own results, at most 2e-8 too small on average for decays up
-        # to 2^-9 below 1 and right on average beyond (csrc/k_scan.cu)
+        # to 2^-9 below 1 and right on average beyond (csrc/k_scan.cuh)
         tol += 2e-8 * min(M, 512)
     return tol
 
