@@ -40,8 +40,8 @@
  *   - Parameters, their gradients and recurrent states are fp32.  Activations
  *     are fp32, bf16 or fp16 (`dtype`), converted exactly to fp32, computed with
  *     in fp32 and rounded once to nearest even.
- *   - Infinite and NaN inputs give what the formulas give (what a length or an absent tensor
- *     leaves out does not count); only dB and dC of zo_scan may be NaN in place of infinite
+ *   - Infinite and NaN inputs give what the formulas give in fp32 (what a length or an absent
+ *     tensor leaves out does not count); only dB and dC of zo_scan may be NaN in place of infinite
  *     where B or C itself is infinite.
  *   - Outputs must not overlap inputs, except where a call says so.
  *   - Results do not depend on timing: no floating-point atomics.
